@@ -9,7 +9,8 @@ from . import binding
 from .binding import (GDN2_BF16, GDN2_FP32, LIB_PATH, STATUS, Gdn2Error, chunk_bwd, chunk_bwd_reduced,
                       chunk_fwd_gated, gdn2_debug_set, GDN2_DEBUG_WAIT_LIMIT, GDN2_DEBUG_WITHHOLD_READY,
                       chunk_bwd_varlen, chunk_fwd, chunk_fwd_reduced, chunk_fwd_varlen, decode_step,
-                      decode_step_reduced, load, output_gate, output_gate_bwd, prologue, prologue_bwd)
+                      decode_step_reduced, load, output_gate, output_gate_bwd, prologue, prologue_bwd,
+                      ssm_bwd, ssm_fwd, ssm_prologue, ssm_prologue_bwd, ssm_prologue_step, ssm_step)
 
 # every C entry point, under its C name
 for _name in binding.SIGNATURES:
@@ -18,5 +19,6 @@ for _name in binding.SIGNATURES:
 __all__ = ["GDN2_BF16", "GDN2_FP32", "LIB_PATH", "STATUS", "Gdn2Error", "chunk_bwd", "chunk_bwd_reduced",
            "chunk_bwd_varlen", "chunk_fwd", "chunk_fwd_reduced", "chunk_fwd_varlen", "decode_step",
            "decode_step_reduced", "load", "chunk_fwd_gated", "GDN2_DEBUG_WAIT_LIMIT", "GDN2_DEBUG_WITHHOLD_READY",
-           "output_gate", "output_gate_bwd", "prologue", "prologue_bwd"] + \
+           "output_gate", "output_gate_bwd", "prologue", "prologue_bwd", "ssm_bwd", "ssm_fwd", "ssm_prologue",
+           "ssm_prologue_bwd", "ssm_prologue_step", "ssm_step"] + \
     list(binding.SIGNATURES)

@@ -22,7 +22,7 @@ STATUS = {0: "GDN2_OK", -1: "GDN2_ERR_INVALID_ARG", -2: "GDN2_ERR_UNSUPPORTED", 
           -4: "GDN2_ERR_TIMEOUT", -5: "GDN2_ERR_WORKSPACE"}
 
 # name -> (restype, argtypes)
-_P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _Z, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 SIGNATURES = {
     "gdn2_version": (_I, []),
     "gdn2_debug_set": (_I, [_I, ctypes.c_longlong]),
@@ -59,6 +59,16 @@ SIGNATURES = {
     "gdn2_output_gate_fwd": (_I, [_P] * 4 + [ctypes.c_longlong, _I, _I, _I, _P]),
     "gdn2_output_gate_bwd_workspace": (_Z, [ctypes.c_longlong, _I, _I]),
     "gdn2_output_gate_bwd": (_I, [_P] * 7 + [ctypes.c_longlong, _I, _I, _I, _P, _Z, _P]),
+    "gdn2_ssm_fwd_workspace": (_Z, [_I] * 8),
+    "gdn2_ssm_states_bytes": (_Z, [_I] * 7),
+    "gdn2_ssm_fwd": (_I, [_P] * 11 + [_L] * 3 + [_I] * 7 + [_P, _Z, _P]),
+    "gdn2_ssm_bwd_workspace": (_Z, [_I] * 9),
+    "gdn2_ssm_bwd": (_I, [_P] * 18 + [_L] * 3 + [_I] * 7 + [_P, _Z, _P]),
+    "gdn2_ssm_step": (_I, [_P] * 8 + [_L] * 3 + [_I] * 6 + [_P]),
+    "gdn2_ssm_prologue_fwd": (_I, [_P] * 3 + [_I] + [_P] * 9 + [_L] * 2 + [_I] * 5 + [_P]),
+    "gdn2_ssm_prologue_bwd_workspace": (_Z, [_I] * 6),
+    "gdn2_ssm_prologue_bwd": (_I, [_P] * 3 + [_I] + [_P] * 15 + [_L] * 2 + [_I] * 5 + [_P, _Z, _P]),
+    "gdn2_ssm_prologue_step": (_I, [_P] * 3 + [_I] + [_P] * 7 + [_L] * 2 + [_I] * 4 + [_P]),
 }
 
 _lib = None
@@ -300,6 +310,64 @@ def gdn2_output_gate_bwd_workspace(rows, H, dv) -> int:
 def gdn2_output_gate_bwd(o, g, gamma, dz, dO, dg, dgamma, rows, H, dv, dtype, ws, ws_bytes, stream=None) -> int:
     return load().gdn2_output_gate_bwd(_ptr(o), _ptr(g), _ptr(gamma), _ptr(dz), _ptr(dO), _ptr(dg), _ptr(dgamma),
                                        rows, H, dv, dtype, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, dtype, packed) -> int:
+    return load().gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, dtype, int(bool(packed)))
+
+
+def gdn2_ssm_states_bytes(B, T, H, dk, dv, dtype, packed) -> int:
+    return load().gdn2_ssm_states_bytes(B, T, H, dk, dv, dtype, int(bool(packed)))
+
+
+def gdn2_ssm_fwd(q, k, v, log_alpha, dt, skip, S0, o, S_T, states, cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk, dv,
+                 dtype, ws, ws_bytes, stream=None) -> int:
+    return load().gdn2_ssm_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(dt), _ptr(skip), _ptr(S0), _ptr(o),
+                               _ptr(S_T), _ptr(states), _ptr(cu_seqlens), ldq, ldk, ldv, B, T, H, G, dk, dv, dtype,
+                               _ptr(ws), ws_bytes, _stream(stream))
+
+
+def gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, dtype, packed, states_given) -> int:
+    return load().gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, dtype, int(bool(packed)), int(bool(states_given)))
+
+
+def gdn2_ssm_bwd(q, k, v, log_alpha, dt, skip, S0, dO, dS_T, states, dq, dk_, dv_, dlog_alpha, ddt, dskip, dS0,
+                 cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk, dv, dtype, ws, ws_bytes, stream=None) -> int:
+    return load().gdn2_ssm_bwd(*map(_ptr, (q, k, v, log_alpha, dt, skip, S0, dO, dS_T, states, dq, dk_, dv_,
+                                           dlog_alpha, ddt, dskip, dS0, cu_seqlens)),
+                               ldq, ldk, ldv, B, T, H, G, dk, dv, dtype, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def gdn2_ssm_step(q, k, v, log_alpha, dt, skip, S, o, ldq, ldk, ldv, B, H, G, dk, dv, dtype, stream=None) -> int:
+    return load().gdn2_ssm_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(dt), _ptr(skip), _ptr(S), _ptr(o),
+                                ldq, ldk, ldv, B, H, G, dk, dv, dtype, _stream(stream))
+
+
+def gdn2_ssm_prologue_fwd(x, W, bias, K, xdt, dt_bias, A_log, init, y, dt, log_alpha, window, cu_seqlens, ldx, ldt,
+                          B, T, C, H, dtype, stream=None) -> int:
+    return load().gdn2_ssm_prologue_fwd(_ptr(x), _ptr(W), _ptr(bias), K,
+                                        *map(_ptr, (xdt, dt_bias, A_log, init, y, dt, log_alpha, window, cu_seqlens)),
+                                        ldx, ldt, B, T, C, H, dtype, _stream(stream))
+
+
+def gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, packed) -> int:
+    return load().gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, int(bool(packed)))
+
+
+def gdn2_ssm_prologue_bwd(x, W, bias, K, xdt, dt_bias, A_log, init, dy, ddt, dlog_alpha, dx, dW, dbias, dxdt,
+                          ddt_bias, dA_log, dinit, cu_seqlens, ldx, ldt, B, T, C, H, dtype, ws, ws_bytes,
+                          stream=None) -> int:
+    return load().gdn2_ssm_prologue_bwd(_ptr(x), _ptr(W), _ptr(bias), K,
+                                        *map(_ptr, (xdt, dt_bias, A_log, init, dy, ddt, dlog_alpha, dx, dW, dbias, dxdt,
+                                                    ddt_bias, dA_log, dinit, cu_seqlens)),
+                                        ldx, ldt, B, T, C, H, dtype, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def gdn2_ssm_prologue_step(x, W, bias, K, xdt, dt_bias, A_log, window, y, dt, log_alpha, ldx, ldt, B, C, H, dtype,
+                           stream=None) -> int:
+    return load().gdn2_ssm_prologue_step(_ptr(x), _ptr(W), _ptr(bias), K,
+                                         *map(_ptr, (xdt, dt_bias, A_log, window, y, dt, log_alpha)), ldx, ldt, B, C, H,
+                                         dtype, _stream(stream))
 
 
 # --------------------------------------------------------------------------
@@ -599,3 +667,286 @@ def chunk_fwd_gated(q, k, v, log_alpha, b, w, g, gamma, S0=None, output_final_st
     _raise(gdn2_chunk_fwd_gated(q, k, v, log_alpha, b, w, S0, g, gamma, z, S_T, B, T, H, dk, dv, dt, ws, nws,
                                 stream), "gdn2_chunk_fwd_gated")
     return z, S_T
+
+
+# --------------------------------------------------------------------------
+# selective state space scan and its prologue
+
+
+class _On:
+    """The device of a call's tensors made current for it, and the stream it
+    runs on: the caller's, or the current one of that device.  Scratch that
+    the call allocates belongs to the device's current stream, so with a
+    stream of the caller's it is recorded there."""
+    __slots__ = ("guard", "stream", "given")
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.given = stream
+        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+
+    def scratch(self, n, device):
+        """n bytes of workspace (None for none)."""
+        import torch
+        if not n:
+            return None
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if self.given is not None:
+            ws.record_stream(self.given if not isinstance(self.given, int)
+                             else torch.cuda.ExternalStream(self.given, device=device))
+        return ws
+
+    def done(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
+
+
+def _row_ld(name, t, lead, width, strides_ok):
+    """Elements between the rows of t [*lead, *inner], whose inner dimensions
+    are contiguous and whose leading ones are rows at one distance."""
+    n = len(lead)
+    if tuple(t.shape[:n]) != tuple(lead) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor with leading dimensions %s, got %s" % (name, tuple(lead), tuple(t.shape)))
+    st, sh = t.stride(), t.shape
+    inner, step = n, 1
+    for d in range(t.dim() - 1, n - 1, -1):
+        if sh[d] != 1 and st[d] != step:
+            raise ValueError("%s must be contiguous within a row" % name)
+        step *= sh[d]
+    # the row distance: that of the last leading dimension longer than one
+    ld = None
+    rows = 1
+    for d in range(n - 1, -1, -1):
+        if sh[d] != 1:
+            if ld is None:
+                ld = st[d] if rows == 1 else None
+            if sh[d] > 1 and ld is not None and st[d] != ld * rows:
+                raise ValueError("%s must have its rows at one distance" % name)
+        rows *= sh[d]
+    if ld is None or t.numel() == 0:
+        ld = width
+    if not strides_ok and ld != width:
+        raise ValueError("%s must be contiguous" % name)
+    return ld
+
+
+def _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, lead_dims):
+    dtype = q.dtype
+    if cu_seqlens is not None:
+        lead_dims = 1
+    lead = tuple(v.shape[:lead_dims])
+    if v.dim() != lead_dims + 2 or q.dim() != lead_dims + 2:
+        raise ValueError("v must be %s + (H, dv) and q, k (G, dk)" % ("[rows]" if lead_dims == 1 else "[B, T]"))
+    H, dv = v.shape[-2:]
+    G, dk = q.shape[-2:]
+    for name, t in (("q", q), ("k", k), ("v", v), ("log_alpha", log_alpha), ("dt", dt)):
+        if t.dtype != dtype or t.device != q.device:
+            raise ValueError("%s must be a CUDA tensor of dtype %s on %s" % (name, dtype, q.device))
+    if tuple(k.shape) != tuple(q.shape) or G < 1 or H % G:
+        raise ValueError("q and k must share a shape [.., G, dk], G dividing H = %d" % H)
+    ldq, ldk, ldv = (_row_ld(n, t, lead, w, True) for n, t, w in (("q", q, G * dk), ("k", k, G * dk), ("v", v, H * dv)))
+    for name, t in (("log_alpha", log_alpha), ("dt", dt)):
+        if tuple(t.shape) != lead + (H,) or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous tensor of shape %s" % (name, lead + (H,)))
+    _check_f32("skip", skip, (H,), q.device)
+    if cu_seqlens is None:
+        B, T = (lead[0], 1) if lead_dims == 1 else lead
+    else:
+        B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
+        if cu_seqlens.device != q.device:
+            raise ValueError("cu_seqlens must be on %s" % q.device)
+    return lead, B, T, H, G, dk, dv, ldq, ldk, ldv
+
+
+def _check_f32(name, t, shape, device):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
+                          t.device != device):
+        raise ValueError("%s must be a contiguous fp32 tensor of shape %s on %s" % (name, shape, device))
+
+
+def _like_rows(t, ld):
+    """An empty tensor with t's shape and row distance."""
+    return t.new_empty(t.shape) if ld == t.shape[-2] * t.shape[-1] else t.new_empty_strided(t.shape, t.stride())
+
+
+def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True, save_states=False, cu_seqlens=None,
+            stream=None):
+    """o, S_T of the selective state space scan S_t = e^{log_alpha_t} S_{t-1} +
+    dt_t k_t v_t^T, o_t = S_t^T q_t + skip v_t.
+
+    v [B, T, H, dv]; q, k [B, T, G, dk], each group read by H / G heads;
+    log_alpha, dt [B, T, H]; skip fp32 [H]; S0 fp32 [B, H, dk, dv].  q, k, v may
+    be views with a longer row stride.  Packed: [rows, ..] tensors and
+    cu_seqlens (B + 1 int32 offsets on the device).  With save_states=True
+    returns (o, S_T, states) for ssm_bwd(..., states=states)."""
+    import torch
+    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
+    code, dev, packed = _dtype_code(q), q.device, cu_seqlens is not None
+    _check_f32("S0", S0, (B, H, dk, dv), dev)
+    on = _On(dev, stream)
+    try:
+        o = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
+        S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
+        states = None
+        if save_states:
+            states = torch.empty(gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed), dtype=torch.uint8, device=dev)
+        nws = gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, code, packed)
+        _raise(gdn2_ssm_fwd(q, k, v, log_alpha, dt, skip, S0, o, S_T, states, cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk,
+                            dv, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_fwd")
+    finally:
+        on.done()
+    return (o, S_T, states) if save_states else (o, S_T)
+
+
+def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=None, need_dS0=True, cu_seqlens=None,
+            into=None, stream=None):
+    """Gradients (dq, dk, dv, dlog_alpha, ddt, dskip, dS0) of ssm_fwd from dO
+    and dS_T.  `states` from ssm_fwd(..., save_states=True) on the same inputs
+    skips forming them anew.  dq, dk, dv have their input's strides; `into`
+    (dq, dk, dv) gives the tensors to write them to, such as views of the
+    prologue's dy."""
+    import torch
+    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
+    code, dev, packed = _dtype_code(q), q.device, cu_seqlens is not None
+    _check_f32("S0", S0, (B, H, dk, dv), dev)
+    _check_f32("dS_T", dS_T, (B, H, dk, dv), dev)
+    if tuple(dO.shape) != lead + (H, dv) or dO.dtype != q.dtype or dO.device != dev or not dO.is_contiguous():
+        raise ValueError("dO must be a contiguous %s tensor of shape %s" % (q.dtype, lead + (H, dv)))
+    if states is not None and (states.dtype != torch.uint8 or states.device != dev or not states.is_contiguous() or
+                               states.numel() != gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed)):
+        raise ValueError("states must be what ssm_fwd(..., save_states=True) returned for these sizes")
+    for name, t, x, ld, w in zip(("dq", "dk", "dv"), into or (), (q, k, v), (ldq, ldk, ldv), (G * dk, G * dk, H * dv)):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != dev or _row_ld(name, t, lead, w, True) != ld:
+            raise ValueError("%s must have its input's shape, dtype and row stride" % name)
+    on = _On(dev, stream)
+    try:
+        dq, dk_, dv_ = into or (_like_rows(q, ldq), _like_rows(k, ldk), _like_rows(v, ldv))
+        g = {"dq": dq, "dk": dk_, "dv": dv_, "dlog_alpha": torch.empty_like(log_alpha),
+             "ddt": torch.empty_like(dt), "dskip": None if skip is None else torch.empty_like(skip),
+             "dS0": torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if need_dS0 else None}
+        nws = gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, code, packed, states is not None)
+        _raise(gdn2_ssm_bwd(q, k, v, log_alpha, dt, skip, S0, dO, dS_T, states, g["dq"], g["dk"], g["dv"],
+                            g["dlog_alpha"], g["ddt"], g["dskip"], g["dS0"], cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk,
+                            dv, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_bwd")
+    finally:
+        on.done()
+    return g
+
+
+def ssm_step(q, k, v, log_alpha, dt, S, skip=None, stream=None):
+    """o = one token of the scan: v [B, H, dv], q, k [B, G, dk], log_alpha, dt
+    [B, H]; S fp32 [B, H, dk, dv] updated in place."""
+    import torch
+    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, None, 1)
+    dev = q.device
+    _check_f32("S", S, (B, H, dk, dv), dev)
+    on = _On(dev, stream)
+    try:
+        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+        _raise(gdn2_ssm_step(q, k, v, log_alpha, dt, skip, S, o, ldq, ldk, ldv, B, H, G, dk, dv, _dtype_code(q),
+                             on.stream), "gdn2_ssm_step")
+    finally:
+        on.done()
+    return o
+
+
+def _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, cu_seqlens, lead_dims):
+    dev = x.device
+    if cu_seqlens is not None:
+        lead_dims = 1
+    lead, C, K = tuple(x.shape[:lead_dims]), x.shape[-1], W.shape[-1]
+    if x.dim() != lead_dims + 1:
+        raise ValueError("x must be %s" % ("[rows, C]" if lead_dims == 1 else "[B, T, C]"))
+    _check_f32("W", W, (C, K), dev)
+    _check_f32("bias", bias, (C,), dev)
+    H, ldt = 0, 0
+    if xdt is not None:
+        H = xdt.shape[-1]
+        if xdt.dtype != x.dtype or xdt.device != dev or xdt.dim() != lead_dims + 1 or A_log is None:
+            raise ValueError("xdt must be a %s tensor %s + (H,) on %s, with A_log" % (x.dtype, lead, dev))
+        ldt = _row_ld("xdt", xdt, lead, H, True)
+        _check_f32("dt_bias", dt_bias, (H,), dev)
+        _check_f32("A_log", A_log, (H,), dev)
+    if cu_seqlens is None:
+        B, T = (lead[0], 1) if lead_dims == 1 else lead
+    else:
+        B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
+        if cu_seqlens.device != dev:
+            raise ValueError("cu_seqlens must be on %s" % dev)
+    if window is not None and (tuple(window.shape) != (B, K - 1, C) or window.dtype != x.dtype or
+                               window.device != dev or not window.is_contiguous()):
+        raise ValueError("the window must be a contiguous %s tensor of shape %s" % (x.dtype, (B, K - 1, C)))
+    return lead, B, T, C, K, H, _row_ld("x", x, lead, C, True), ldt
+
+
+def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False, cu_seqlens=None, stream=None):
+    """(y, dt, log_alpha, window): y = silu(conv(x) + bias) [B, T, C] with
+    filters W fp32 [C, K], dt = softplus(xdt + dt_bias) and log_alpha =
+    -exp(A_log) dt [B, T, H] (xdt None: neither).  init [B, K-1, C]: the inputs
+    before each sequence (None: zeros); window: those before its next token
+    (None without output_window).  Packed: [rows, ..] and cu_seqlens."""
+    import torch
+    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
+    code, dev = _dtype_code(x), x.device
+    on = _On(dev, stream)
+    try:
+        y = torch.empty(lead + (C,), dtype=x.dtype, device=dev)
+        dt = la = None
+        if H:
+            dt, la = (torch.empty(lead + (H,), dtype=x.dtype, device=dev) for _ in range(2))
+        window = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if output_window else None
+        _raise(gdn2_ssm_prologue_fwd(x, W, bias, K, xdt, dt_bias, A_log, init, y, dt, la, window, cu_seqlens, ldx, ldt,
+                                     B, T, C, H, code, on.stream), "gdn2_ssm_prologue_fwd")
+    finally:
+        on.done()
+    return y, dt, la, window
+
+
+def ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt=None, dlog_alpha=None, init=None, cu_seqlens=None,
+                     stream=None):
+    """Gradients of ssm_prologue from dy, ddt and dlog_alpha: dx, dW, dbias,
+    dxdt, ddt_bias, dA_log and, with init, dinit (None for what was not given)."""
+    import torch
+    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
+    code, dev = _dtype_code(x), x.device
+    for name, t, w in (("dy", dy, C), ("ddt", ddt, H), ("dlog_alpha", dlog_alpha, H)):
+        if w and (t is None or tuple(t.shape) != lead + (w,) or t.dtype != x.dtype or t.device != dev or
+                  not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, x.dtype, lead + (w,)))
+    on = _On(dev, stream)
+    try:
+        g = {"dx": torch.empty(lead + (C,), dtype=x.dtype, device=dev), "dW": torch.empty_like(W)}
+        g.update({n: None if t is None else torch.empty_like(t) for n, t in (("dbias", bias), ("dinit", init))})
+        g.update({n: None if t is None or not H else torch.empty_like(t) for n, t in
+                  (("ddt_bias", dt_bias), ("dA_log", A_log))})
+        g["dxdt"] = torch.empty(lead + (H,), dtype=x.dtype, device=dev) if H else None
+        nws = gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, cu_seqlens is not None)
+        _raise(gdn2_ssm_prologue_bwd(x, W, bias, K, xdt, dt_bias, A_log, init, dy, ddt, dlog_alpha, g["dx"], g["dW"],
+                                     g["dbias"], g["dxdt"], g["ddt_bias"], g["dA_log"], g["dinit"], cu_seqlens, ldx, ldt,
+                                     B, T, C, H, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_prologue_bwd")
+    finally:
+        on.done()
+    return g
+
+
+def ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream=None):
+    """(y, dt, log_alpha) of one token per sequence: x [B, C], xdt [B, H]
+    (None: only y); window [B, K-1, C] updated in place."""
+    import torch
+    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, None, 1)
+    dev = x.device
+    on = _On(dev, stream)
+    try:
+        y = torch.empty((B, C), dtype=x.dtype, device=dev)
+        dt = la = None
+        if H:
+            dt, la = (torch.empty((B, H), dtype=x.dtype, device=dev) for _ in range(2))
+        _raise(gdn2_ssm_prologue_step(x, W, bias, K, xdt, dt_bias, A_log, window, y, dt, la, ldx, ldt, B, C, H,
+                                      _dtype_code(x), on.stream), "gdn2_ssm_prologue_step")
+    finally:
+        on.done()
+    return y, dt, la

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "launch.h"
+#include "ssm.h"
 
 namespace gdn2 {
 
@@ -71,6 +72,9 @@ int copy_state(float *dst, const float *src, int B, int H, int dk, int dv, cudaS
 }
 
 }  // namespace
+
+int *device_status_ptr() { return status_ptr(); }
+
 }  // namespace gdn2
 
 using namespace gdn2;

@@ -333,6 +333,96 @@ int gdn2_output_gate_bwd(const void *o, const void *g, const float *gamma, const
                          void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Selective state space scan: the linear recurrence with a scalar decay per
+ * token and head and no erase,
+ *
+ *     S_t = e^{log_alpha_t} S_{t-1} + dt_t k_t v_t^T,   o_t = S_t^T q_t + skip_h v_t
+ *
+ * (q = C, k = B, v = x and skip = D in the usual names of a state space
+ * layer).  v and o have H heads of dv channels; q and k have G heads of dk
+ * channels, G dividing H, head h reading group h / (H / G).  log_alpha and dt
+ * are [.., H] in the token dtype, skip fp32 [H] or null (no such term).
+ *
+ * Rows of q, k and v lie ldq, ldk and ldv elements apart (heads side by side
+ * within a row), so that they may be views of one wider tensor, such as the
+ * prologue's output; a fixed-length batch's sequences are T rows apart.  o, dO,
+ * log_alpha and dt are contiguous.  q, k, v are 16-byte aligned, their row
+ * strides a multiple of 16 bytes and at least their width; log_alpha and dt
+ * need element alignment.  States are fp32 [B, H, dk, dv].  Sequences: B of T
+ * tokens, or (cu_seqlens != null) a packed batch of B sequences in T rows, as
+ * for the _varlen calls; rows of no sequence are left as they were, and a
+ * sequence whose offsets are out of range is skipped, with
+ * GDN2_ERR_INVALID_ARG in the device status word.
+ *
+ * gdn2_ssm_fwd: o, S_T (null: not wanted), and where `states` is not null
+ * (gdn2_ssm_states_bytes(...) bytes) what gdn2_ssm_bwd wants from the forward,
+ * in a layout private to the library.  gdn2_ssm_bwd: the gradients of every
+ * input from dO and dS_T (null = zero): dq, dk_, dv_ with the row strides of q,
+ * k, v; dlog_alpha and ddt [.., H]; dskip fp32 [H] and dS0 fp32 (null: not
+ * wanted).  q's and k's gradients are sums over the heads of a group, dskip's
+ * over every token, all in a fixed order.  `states` null: formed anew, in a
+ * larger workspace (states_given = 0 in its query).  The workspace queries
+ * take the same sizes, with packed != 0 for a packed batch, and hold for the
+ * device that is current; no workspace may be shared by calls that overlap.
+ * An empty sequence hands its state through; T = 0 likewise.
+ *
+ * gdn2_ssm_step: one token per sequence, rows [B], S updated in place.
+ */
+size_t gdn2_ssm_fwd_workspace(int B, int T, int H, int G, int dk, int dv, int dtype, int packed);
+size_t gdn2_ssm_states_bytes(int B, int T, int H, int dk, int dv, int dtype, int packed);
+int gdn2_ssm_fwd(const void *q, const void *k, const void *v, const void *log_alpha, const void *dt,
+                 const float *skip, const float *S0, void *o, float *S_T, void *states, const int *cu_seqlens,
+                 long long ldq, long long ldk, long long ldv, int B, int T, int H, int G, int dk, int dv, int dtype,
+                 void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t gdn2_ssm_bwd_workspace(int B, int T, int H, int G, int dk, int dv, int dtype, int packed, int states_given);
+int gdn2_ssm_bwd(const void *q, const void *k, const void *v, const void *log_alpha, const void *dt,
+                 const float *skip, const float *S0, const void *dO, const float *dS_T, const void *states, void *dq,
+                 void *dk_, void *dv_, void *dlog_alpha, void *ddt, float *dskip, float *dS0, const int *cu_seqlens,
+                 long long ldq, long long ldk, long long ldv, int B, int T, int H, int G, int dk, int dv, int dtype,
+                 void *ws, size_t ws_bytes, cudaStream_t stream);
+int gdn2_ssm_step(const void *q, const void *k, const void *v, const void *log_alpha, const void *dt,
+                  const float *skip, float *S, void *o, long long ldq, long long ldk, long long ldv, int B, int H,
+                  int G, int dk, int dv, int dtype, cudaStream_t stream);
+
+/*
+ * The prologue of a state space layer: a depthwise causal convolution over K
+ * taps (1..4) with bias and SiLU on C channels (a multiple of 8), and the
+ * step size and log decay of H heads,
+ *
+ *     y[t, c] = silu(bias[c] + sum_j W[c][j] x[t - (K-1) + j, c])
+ *     dt = log(1 + exp(xdt + dt_bias)),   log_alpha = -exp(A_log) dt
+ *
+ * (either part is left out with C = 0 or H = 0).  x and xdt are in the token
+ * dtype, their rows ldx and ldt elements apart, element-aligned (16-byte
+ * alignment of x and ldx is faster); W fp32 [C][K], bias fp32 [C] or null,
+ * dt_bias fp32 [H] or null, A_log fp32 [H].  y [.., C] (16-byte aligned), dt and
+ * log_alpha [.., H] are contiguous.  The taps before a sequence's first token
+ * read its window `init` [B, K-1, C] (null: zeros); `window` (null: not
+ * wanted) receives the K - 1 inputs before the token after its last, so that
+ * a later call or gdn2_ssm_prologue_step continues from it; the two may not
+ * overlap.  Sequences as for the scan.
+ *
+ * gdn2_ssm_prologue_bwd: dx [.., C] and dxdt [.., H] (contiguous), dinit (null:
+ * not wanted; no gradient is taken through `window`), and fp32 dW, dbias,
+ * ddt_bias (null: not wanted) and dA_log, sums over every token in a fixed
+ * order.  gdn2_ssm_prologue_step: one token per sequence; the window is
+ * updated in place.
+ */
+int gdn2_ssm_prologue_fwd(const void *x, const float *W, const float *bias, int K, const void *xdt,
+                          const float *dt_bias, const float *A_log, const void *init, void *y, void *dt,
+                          void *log_alpha, void *window, const int *cu_seqlens, long long ldx, long long ldt, int B,
+                          int T, int C, int H, int dtype, cudaStream_t stream);
+size_t gdn2_ssm_prologue_bwd_workspace(int B, int T, int C, int K, int H, int packed);
+int gdn2_ssm_prologue_bwd(const void *x, const float *W, const float *bias, int K, const void *xdt,
+                          const float *dt_bias, const float *A_log, const void *init, const void *dy, const void *ddt,
+                          const void *dlog_alpha, void *dx, float *dW, float *dbias, void *dxdt, float *ddt_bias,
+                          float *dA_log, void *dinit, const int *cu_seqlens, long long ldx, long long ldt, int B,
+                          int T, int C, int H, int dtype, void *ws, size_t ws_bytes, cudaStream_t stream);
+int gdn2_ssm_prologue_step(const void *x, const float *W, const float *bias, int K, const void *xdt,
+                           const float *dt_bias, const float *A_log, void *window, void *y, void *dt, void *log_alpha,
+                           long long ldx, long long ldt, int B, int C, int H, int dtype, cudaStream_t stream);
+
+/*
  * gdn2_chunk_fwd without a caller-provided workspace, for callers that cannot
  * allocate device memory (no cudaMalloc available to them, or a code path
  * that must not allocate).  The pages have no counterpart to this call; it is
