@@ -16,7 +16,7 @@ int device_sm_count();     // SMs of the current device
 
 namespace ssm {
 
-constexpr int kC = 64;  // chunk of the fp32 kernels, and the unit of their state slots
+constexpr int kC = 64;  // tokens of a chunk of the fp32 kernels (the bf16 ones: 128)
 
 // Where sequence b's tokens lie; chunks of CH tokens.  Fixed length (cu ==
 // nullptr): rows b*T .. ; packed: rows cu[b] .. cu[b+1] - 1 of T rows in all.
@@ -103,7 +103,13 @@ struct ScanBwdArgs {
     float *dskip_part;   // [slots][H]
 };
 
-// ssm_scan.cu (fp32)
+// ssm_scan_tc.cu, ssm_bwd_tc.cu (bf16); grads: the chain of a.grads alone
+cudaError_t launch_scan_fwd_tc(const ScanArgs &a, int dk, int dv, cudaStream_t s);
+cudaError_t launch_scan_grads_tc(const ScanBwdArgs &a, int dk, int dv, cudaStream_t s);
+cudaError_t launch_scan_bwd_tc(const ScanBwdArgs &a, int dk, int dv, cudaStream_t s);
+
+// ssm_scan.cu (fp32); sums: dq, dk from the splits' and dskip from the chunks'
+cudaError_t launch_grad_sums(const ScanBwdArgs &a, int dk, bool bf16, int chunk, cudaStream_t s);
 cudaError_t launch_scan_fwd_f32(const ScanArgs &a, int dk, int dv, cudaStream_t s);
 cudaError_t launch_scan_bwd_f32(const ScanBwdArgs &a, int dk, int dv, cudaStream_t s);
 

@@ -52,14 +52,17 @@ bool ld_ok(long long ld, int width, int dtype) { return ld >= width && ld % (dty
 size_t r256(size_t x) { return (x + 255) / 256 * 256; }
 long long rows_of(const void *cu, int B, int T) { return cu ? (long long)T : (long long)B * T; }
 
-// Parts a sequence is cut into: enough that the parts of all sequences fill
-// the SMs' `slots` once, each at least four chunks long (a part costs its
-// tokens once more for its end state).
-int part_count(const void *cu, int B, int T, int H, int blocks_per_seq, int chunk) {
+int chunk_of(int dtype) { return dtype == GDN2_BF16 ? 128 : kC; }
+
+// Parts a sequence is cut into: as many as fill the SMs (bf16: a block of the
+// walk takes a whole SM; fp32: two of its 64-column blocks share one), each at
+// least four chunks long, for a part costs its tokens once more for its end state.
+int part_count(const void *cu, int B, int T, int H, int dv, int dtype) {
     if (B == 0 || H == 0) return 1;
-    const long long slots = 2LL * device_sm_count(), seqs = (long long)B * H * blocks_per_seq;
-    const long long chunks = cu ? (T / B + chunk - 1) / chunk : (T + chunk - 1) / chunk;
-    const long long p = std::min(slots / std::max(1LL, seqs), chunks / 4);
+    const long long room = (long long)device_sm_count() * (dtype == GDN2_BF16 ? 1 : 2);
+    const long long blocks = (long long)B * H * (dtype == GDN2_BF16 ? 1 : dv / 64);
+    const long long chunks = ((cu ? T / B : T) + chunk_of(dtype) - 1) / chunk_of(dtype);
+    const long long p = std::min(room / std::max(1LL, blocks), chunks / 4);
     return (int)std::max(1LL, std::min(p, 64LL));
 }
 
@@ -70,9 +73,10 @@ struct Plan {
 
 Plan plan(const void *cu, int B, int T, int H, int G, int dk, int dv, int dtype, bool bwd, bool own_states) {
     Plan p{};
-    const size_t SE = (size_t)dk * dv;
-    const long long slots = slot_count(cu, B, T, kC), rows = rows_of(cu, B, T);
-    p.parts = part_count(cu, B, T, H, dv / 64, kC);
+    const size_t SE = (size_t)dk * dv, img = SE * (dtype == GDN2_BF16 ? 2 : 4);
+    const int chunk = chunk_of(dtype);
+    const long long slots = slot_count(cu, B, T, chunk), rows = rows_of(cu, B, T);
+    p.parts = part_count(cu, B, T, H, dv, dtype);
     size_t at = 0;
     p.part_state = at; at += r256((size_t)B * H * (p.parts - 1) * SE * 4);
     p.part_decay = at; at += r256((size_t)B * H * (p.parts - 1) * 4);
@@ -81,8 +85,8 @@ Plan plan(const void *cu, int B, int T, int H, int G, int dk, int dv, int dtype,
         const int hpg = H / G;
         while (p.splits < hpg && slots * G * p.splits < 2LL * device_sm_count()) p.splits *= 2;
         p.splits = std::min(p.splits, hpg);
-        p.grads = at; at += r256((size_t)slots * H * SE * 4);
-        p.states = at; at += own_states ? r256((size_t)slots * H * SE * 4) : 0;
+        p.grads = at; at += r256((size_t)slots * H * img);
+        p.states = at; at += own_states ? r256((size_t)slots * H * img) : 0;
         p.dqk = at; at += p.splits > 1 ? r256((size_t)2 * p.splits * rows * G * dk * 4) : 0;
         p.dskip = at; at += r256((size_t)slots * H * 4);
     }
@@ -117,7 +121,7 @@ extern "C" {
 
 size_t gdn2_ssm_states_bytes(int B, int T, int H, int dk, int dv, int dtype, int packed) {
     if (check(B, T, H, 1, dk, dv, dtype) != GDN2_OK || B == 0 || T == 0 || H == 0) return 0;
-    return (size_t)slot_count(packed_mark(packed), B, T, kC) * H * dk * dv * 4;
+    return (size_t)slot_count(packed_mark(packed), B, T, chunk_of(dtype)) * H * dk * dv * (dtype == GDN2_BF16 ? 2 : 4);
 }
 
 size_t gdn2_ssm_fwd_workspace(int B, int T, int H, int G, int dk, int dv, int dtype, int packed) {
@@ -149,8 +153,7 @@ int gdn2_ssm_fwd(const void *q, const void *k, const void *v, const void *log_al
     unsigned char *w = static_cast<unsigned char *>(ws);
     a.part_state = reinterpret_cast<float *>(w + p.part_state);
     a.part_decay = reinterpret_cast<float *>(w + p.part_decay);
-    if (dtype == GDN2_BF16) return GDN2_ERR_UNSUPPORTED;
-    return launch_status(launch_scan_fwd_f32(a, dk, dv, stream));
+    return launch_status(dtype == GDN2_BF16 ? launch_scan_fwd_tc(a, dk, dv, stream) : launch_scan_fwd_f32(a, dk, dv, stream));
 }
 
 int gdn2_ssm_bwd(const void *q, const void *k, const void *v, const void *log_alpha, const void *dt,
@@ -185,12 +188,11 @@ int gdn2_ssm_bwd(const void *q, const void *k, const void *v, const void *log_al
     a.dskip = dskip; a.dS0 = dS0; a.grads = w + p.grads; a.splits = p.splits;
     a.dqk_part = reinterpret_cast<float *>(w + p.dqk);
     a.dskip_part = reinterpret_cast<float *>(w + p.dskip);
-    if (dtype == GDN2_BF16) return GDN2_ERR_UNSUPPORTED;
     if (!states) {  // the states at the chunks' starts, without o
-        const cudaError_t e = launch_scan_fwd_f32(a.f, dk, dv, stream);
+        const cudaError_t e = dtype == GDN2_BF16 ? launch_scan_fwd_tc(a.f, dk, dv, stream) : launch_scan_fwd_f32(a.f, dk, dv, stream);
         if (e != cudaSuccess) return launch_status(e);
     }
-    return launch_status(launch_scan_bwd_f32(a, dk, dv, stream));
+    return launch_status(dtype == GDN2_BF16 ? launch_scan_bwd_tc(a, dk, dv, stream) : launch_scan_bwd_f32(a, dk, dv, stream));
 }
 
 int gdn2_ssm_step(const void *q, const void *k, const void *v, const void *log_alpha, const void *dt,

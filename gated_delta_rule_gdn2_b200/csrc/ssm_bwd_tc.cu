@@ -1,0 +1,559 @@
+// The selective state space scan's gradients of a chunk, for bf16 tokens on
+// the fifth-generation tensor cores.
+//
+// A CTA takes one chunk of 128 tokens of one group (or of a run of its heads)
+// and goes through the heads, 64 value columns at a time ("a unit": v, dO and
+// the matching columns of the state S at the chunk's start and of the gradient
+// E at its end, 64 KB, double buffered).  With the factors of ssm_scan.cu,
+// G = q k^T kept once per CTA and D_ij the decay from j to i, a unit is
+//     X = v dO^T            -> W = G D X: sums for dla and ddt; Z += D X dt
+//     Y = k E               -> r_j = w_j Y_j . v_j; Y scaled by w_j
+//     Y += (G D)^T dO       -> dv = dt Y + skip dO
+//     U = dO S^T            -> dq += e^L U (registers); u_i = e^{L_i} q_i . U_i
+//     dk += (dt w v) E^T
+// and behind the last head dq += Z k, dk += Z^T q, so that both are summed over
+// the heads before they are rounded.  Rows of X, Y are tokens j (lanes of
+// tensor memory), columns i, so that (G D)^T is written back to tensor memory
+// as the left operand of the third product; the sums over j of W's columns are
+// a transposing reduction within each warp.  Operands rounded to bf16: G, G D,
+// dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
+//
+// Bound: 64 KB in and 16 KB out a unit at dk = 128 against 1500 cycles of
+// tensor pipe and about as many of the warps' arithmetic.
+#include "common.cuh"
+#include "ssm_tc.cuh"
+
+namespace gdn2 {
+namespace ssm {
+namespace {
+
+using tct::mma_tiles;
+
+struct BwdMaps {
+    CUtensorMap q, k, v, dO, dv;
+};
+
+// As Gates, but without dt in cf and wt, and with lf = e^l.
+struct alignas(16) BwdGates {
+    float l[kCT], lf[kCT], cf[kCT], er[kCT], wt[kCT], dt[kCT];
+    float bs[4];
+    float gamma;
+};
+__device__ __forceinline__ void form_bwd_gates(BwdGates &g, float la, float dt, int t) {
+    const int lane = t & 31, w = t >> 5;
+    float up = la, dn = la;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, up, m), z = __shfl_down_sync(0xffffffffu, dn, m);
+        if (lane >= m) up += y;
+        if (lane + m < 32) dn += z;
+    }
+    const float behind = __shfl_down_sync(0xffffffffu, dn, 1), s = lane < 31 ? behind : 0.f;
+    g.l[t] = up;
+    g.lf[t] = __expf(up);
+    g.cf[t] = __expf(s);
+    g.dt[t] = dt;
+    if (lane == 31) g.bs[w] = up;
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");
+    const float b0 = g.bs[0], b1 = g.bs[1], b2 = g.bs[2], b3 = g.bs[3];
+    const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
+    const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
+    g.er[t] = __expf(pre + up);
+    g.wt[t] = __expf(s + post);
+    if (t == 0) g.gamma = __expf(b0 + b1 + b2 + b3);
+}
+
+// Sums over the 32 lanes of 16 values a lane: lanes 2 c and 2 c + 1 end with
+// the sum of value c (each step keeps the upper half where the lane's bit m is set).
+__device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
+#pragma unroll
+    for (int n = 8, m = 16; n >= 1; n >>= 1, m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+    }
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+template <int N>
+struct BwdTcSmem {
+    static constexpr int QB = kCT * N * 2, VB = kCT * 64 * 2, SB = N * 64 * 2, STAGE = 2 * VB + 2 * SB;
+    static constexpr int K = 0, Q = QB, ST0 = 2 * QB, STG = ST0 + 2 * STAGE, G = STG + VB,
+                         ROWP = G + 2 * (int)sizeof(BwdGates), COLP = ROWP + 4 * kCT * 4, RP = COLP + 4 * kCT * 4,
+                         UP = RP + 4 * kCT * 4, CD = UP + 4 * kCT * 4, RED = CD + kCT * 4, END = RED + 2 * 16 * 4;
+    static constexpr int BYTES = END + 1024;
+    static_assert(BYTES + 128 <= 232448, "shared memory of an SM");
+};
+
+template <int N, int P>
+__global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid_constant__ BwdMaps maps) {
+    using L = BwdTcSmem<N>;
+    constexpr int NX = P / 64, WN = N / 4;  // units a head; a thread's columns of an N-column row
+    constexpr uint32_t cX = 0, cY = 128, cDK = 192, cA = 320, cG = 384;
+    constexpr uint32_t idX = tc::idesc_bf16(128, 128, false, false), idY = tc::idesc_bf16(128, 64, false, true),
+                       idN = tc::idesc_bf16(128, N, false, false), idZk = tc::idesc_bf16(128, N, false, true),
+                       idZq = tc::idesc_bf16(128, N, true, true);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
+    __shared__ uint64_t ld_qk, ld[2], b_x, b_y, b_c, b_d, b_e, b_z;
+    __shared__ uint32_t tmem_slot;
+    BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
+    float(*rowp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::ROWP), (*colp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::COLP);
+    float(*rp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::RP), (*up)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::UP);
+    float *cd = reinterpret_cast<float *>(sm + L::CD), *red = reinterpret_cast<float *>(sm + L::RED);
+    const ScanArgs &f = a.f;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, qc = warp >> 2, row = 32 * p + lane;
+    const int hpg = f.H / f.G, per = (hpg + a.splits - 1) / a.splits;
+    const int sp = blockIdx.x % a.splits, g = (blockIdx.x / a.splits) % f.G;
+    const long long slot = blockIdx.x / (a.splits * f.G);
+    const int h_lo = g * hpg + min(sp * per, hpg), nh = g * hpg + min((sp + 1) * per, hpg) - h_lo, nu = nh * NX;
+    int b, n;
+    Seq sq;
+    if (!find_slot(f.cu, f.B, f.T, kCT, slot, b, n, sq)) {
+        if (a.dskip_part)
+            for (int i = tid; i < nh; i += kNT) a.dskip_part[slot * f.H + h_lo + i] = 0.f;
+        return;
+    }
+    const int t0 = n * kCT, len = min(kCT, sq.len - t0);
+    const size_t grow = (size_t)(sq.row0 + t0);  // the chunk's first row
+    const int mb = f.cu ? 0 : b, mt = (f.cu ? (int)sq.row0 : 0) + t0;
+    const bool tail = f.cu && len < kCT;
+
+    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+    if (tid == 0) {
+        uint64_t *bars[] = {&ld_qk, &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_e, &b_z};
+        for (uint64_t *x : bars) tc::mbar_init(x, 1);
+        tc::fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
+
+    int nl[2] = {0, 0};
+    auto load = [&](int u) {
+        const int s = u & 1, h = h_lo + u / NX, x = u % NX;
+        unsigned char *st = sm + L::ST0 + s * L::STAGE;
+        tc::mbar_expect_tx(&ld[s], L::STAGE);
+        tc::tma_load_5d(st, &maps.v, 0, mt, x, h, mb, &ld[s]);
+        tc::tma_load_5d(st + L::VB, &maps.dO, 0, mt, x, h, mb, &ld[s]);
+        const size_t img = ((size_t)slot * f.H + h) * (N * P * 2) + (size_t)x * L::SB;
+        tc::bulk_load(st + 2 * L::VB, static_cast<const unsigned char *>(a.grads) + img, L::SB, &ld[s]);
+        tc::bulk_load(st + 2 * L::VB + L::SB, static_cast<const unsigned char *>(f.states) + img, L::SB, &ld[s]);
+        ++nl[s];
+    };
+    bool bad = false, aborted = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!tc::mbar_wait(bar, parity)) {
+            bad = true;
+            record_status(f.status, GDN2_ERR_TIMEOUT);
+        }
+    };
+    auto handoff = [&]() {
+        tc::fence_async_smem();
+        tc::fence_before();
+        aborted = __syncthreads_or(bad);
+        tc::fence_after();
+    };
+    if (tid == 0) {
+        tc::mbar_expect_tx(&ld_qk, 2 * L::QB);
+        for (int x = 0; x < N / 64; ++x) {
+            tc::tma_load_5d(sm + L::K + x * kCT * 128, &maps.k, 0, mt, x, g, mb, &ld_qk);
+            tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt, x, g, mb, &ld_qk);
+        }
+        if (nu > 0) load(0);
+        if (nu > 1) load(1);
+    }
+    // the last four warps form the decay factors, one head ahead
+    float g_la = 0.f, g_dt = 0.f;
+    const int gt = tid - (kNT - kCT);
+    auto load_gates = [&](int i) {
+        g_la = g_dt = 0.f;
+        if (i < nh && gt < len) {
+            const size_t r = (grow + gt) * f.H + h_lo + i;
+            g_la = fmaxf(__bfloat162float(static_cast<const bf16 *>(f.la)[r]), kLogMin);
+            g_dt = __bfloat162float(static_cast<const bf16 *>(f.dt)[r]);
+        }
+    };
+    if (gt >= 0) {
+        load_gates(0);
+        form_bwd_gates(gates[0], g_la, g_dt, gt);
+        load_gates(1);
+    }
+    for (int i = tid; i < 16 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp, colp, rp, up lie side by side)
+
+    // ---- G^T = k q^T, kept as bf16 pairs in tensor memory
+    wait(&ld_qk, 0);
+    if (tail) {
+        zero_tail(sm + L::K, N / 64, len, tid, kNT);
+        zero_tail(sm + L::Q, N / 64, len, tid, kNT);
+    }
+    handoff();
+    if (tid == 0) {
+        mma_tiles<true, true>(tm + cX, sm + L::K, kCT, sm + L::Q, kCT, N / 16, idX, false);
+        tc::commit(&b_z);
+    }
+    wait(&b_z, 0);
+    tc::fence_after();
+    {
+        float x[32];
+        uint32_t u[16];
+        tc::ld_32x32b_x32(tl + cX + 32 * qc, x);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
+        st16(tl + cG + 16 * qc, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = 0u;
+        st16(tl + cA + 16 * qc, u);  // (blocks i < j of (G D)^T stay zero)
+        tc::wait_st();
+    }
+    handoff();
+
+    float Z[32], dq[WN], es = 0.f, dsk = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) Z[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < WN; ++i) dq[i] = 0.f;
+
+    for (int u = 0; u < nu && !aborted; ++u) {
+        const int s = u & 1, hh = u / NX, x = u % NX, h = h_lo + hh;
+        const uint32_t ph = u & 1, ph2 = (u >> 1) & 1;
+        const BwdGates &G = gates[hh & 1];
+        unsigned char *sV = sm + L::ST0 + s * L::STAGE, *sO = sV + L::VB, *sE = sO + L::VB, *sS = sE + L::SB;
+        wait(&ld[s], ph2);
+        if (tail) {
+            zero_tail(sV, 1, len, tid, kNT);
+            zero_tail(sO, 1, len, tid, kNT);
+            handoff();
+            if (aborted) break;
+        }
+        if (tid == 0) {
+            mma_tiles<true, true>(tm + cX, sV, kCT, sO, kCT, 4, idX, false);
+            tc::commit(&b_x);
+            mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
+            tc::commit(&b_y);
+            if (u > 0 && u + 1 < nu) {  // the other stage: free once its last product is done
+                wait(&b_e, (u - 1) & 1);
+                load(u + 1);
+            }
+        }
+        const float dtj = G.dt[row];
+        // <E, S> (the two images have one layout)
+#pragma unroll
+        for (int i = 0; i < L::SB / 16 / kNT; ++i) {
+            const uint4 e = reinterpret_cast<const uint4 *>(sE)[tid + i * kNT], t = reinterpret_cast<const uint4 *>(sS)[tid + i * kNT];
+            const uint32_t ee[4] = {e.x, e.y, e.z, e.w}, tt[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 y = unpack2(ee[c]), z = unpack2(tt[c]);
+                es = fmaf(y.x, z.x, fmaf(y.y, z.y, es));
+            }
+        }
+        if (u > 0 && x == 0) asm volatile("bar.sync 2, 512;\n" ::: "memory");  // the head before is summed up
+        wait(&b_x, ph);
+        tc::fence_after();
+        // ---- X: token j = row, tokens i = 32 qc ..
+        if (qc >= p) {
+            const float lj = G.l[row];
+            const float fj = qc > p ? G.cf[row] * __expf(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]) : 0.f;
+            float col = 0.f;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float X[16], w[16];
+                uint32_t gp[8];
+                ld16(tl + cX + 32 * qc + 16 * hf, X);
+                ld8(tl + cG + 16 * qc + 8 * hf, gp);
+                tc::wait_ld();
+                uint32_t am[8];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 gg = unpack2(gp[i / 2]);
+                    float d0, d1;
+                    const int i0 = 16 * hf + i;  // within the block
+                    if (qc > p) {
+                        const float2 lf = *reinterpret_cast<const float2 *>(&G.lf[32 * qc + i0]);
+                        d0 = lf.x * fj;
+                        d1 = lf.y * fj;
+                    } else {
+                        const float2 l2 = *reinterpret_cast<const float2 *>(&G.l[32 * qc + i0]);
+                        d0 = i0 >= lane ? __expf(l2.x - lj) : 0.f;
+                        d1 = i0 + 1 >= lane ? __expf(l2.y - lj) : 0.f;
+                    }
+                    const float x0 = X[i] * d0, x1 = X[i + 1] * d1;
+                    Z[i0] = fmaf(x0, dtj, Z[i0]);
+                    Z[i0 + 1] = fmaf(x1, dtj, Z[i0 + 1]);
+                    am[i / 2] = pack2(gg.x * d0, gg.y * d1);
+                    float w0 = gg.x * x0, w1 = gg.y * x1;
+                    if (qc == p) {  // the diagonal apart: it is in ddt, not in dla
+                        if (i0 == lane) { cd[row] = x == 0 ? w0 : cd[row] + w0; w0 = 0.f; }
+                        if (i0 + 1 == lane) { cd[row] = x == 0 ? w1 : cd[row] + w1; w1 = 0.f; }
+                    }
+                    col += w0 + w1;
+                    w[i] = w0 * dtj;
+                    w[i + 1] = w1 * dtj;
+                }
+                st8(tl + cA + 16 * qc + 8 * hf, am);
+                const float rs = lane_sums16(w, lane);
+                if ((lane & 1) == 0) {
+                    float *dst = &rowp[p][32 * qc + 16 * hf + (lane >> 1)];
+                    *dst = x == 0 ? rs : *dst + rs;
+                }
+            }
+            colp[qc][row] = x == 0 ? col : colp[qc][row] + col;
+        }
+        // ---- Y: token j = row, value columns 16 qc ..
+        wait(&b_y, ph);
+        tc::fence_after();
+        {
+            float y[16];
+            ld16(tl + cY + 16 * qc, y);
+            const float w = G.wt[row], wd = w * dtj;
+            tc::wait_ld();
+            float r = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = piece(kCT, row, 2 * qc + i);
+                const uint4 v = *reinterpret_cast<const uint4 *>(sV + at), o = *reinterpret_cast<const uint4 *>(sO + at);
+                uint32_t ve[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 vv = unpack2(ve[e]), oo = unpack2(oe[e]);
+                    const int c = 8 * i + 2 * e;
+                    dsk = fmaf(vv.x, oo.x, fmaf(vv.y, oo.y, dsk));
+                    y[c] *= w;
+                    y[c + 1] *= w;
+                    r = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, r));
+                    ve[e] = pack2(vv.x * wd, vv.y * wd);
+                }
+                *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
+            }
+            stw<16>(tl + cY + 16 * qc, y);
+            rp[qc][row] = x == 0 ? r : rp[qc][row] + r;
+            tc::wait_st();
+        }
+        if (x == NX - 1) {
+            const float e2 = warp_sum(es), d2 = warp_sum(dsk);
+            if (lane == 0) {
+                red[warp] = e2;
+                red[16 + warp] = d2;
+            }
+            es = dsk = 0.f;
+        }
+        if (x == 0 && gt >= 0) {
+            form_bwd_gates(gates[(hh + 1) & 1], g_la, g_dt, gt);
+            load_gates(hh + 2);
+        }
+        if (tid == 0) tc::bulk_wait_read();  // the dv tile of the unit before
+        handoff();
+        if (aborted) break;
+        if (tid == 0) {
+            const uint64_t o0 = tct::mnmaj(sO, kCT, 0);
+#pragma unroll
+            for (int i = 0; i < kCT / 16; ++i)
+                mma_ts(tm + cY, tm + cA + 8 * i, o0 + (tct::kstep_bytes<false>(kCT, i) >> 4), idY, true);
+            tc::commit(&b_c);
+            mma_tiles<true, true>(tm + cX, sO, kCT, sS, N, 4, idN, false);
+            tc::commit(&b_d);
+            mma_tiles<true, true>(tm + cDK, sV, kCT, sE, N, 4, idN, u > 0);
+            tc::commit(&b_e);
+        }
+        wait(&b_c, ph);
+        tc::fence_after();
+        {  // dv
+            float y[16];
+            ld16(tl + cY + 16 * qc, y);
+            const float skip = f.skip ? f.skip[h] : 0.f;
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = piece(kCT, row, 2 * qc + i);
+                const uint4 o = *reinterpret_cast<const uint4 *>(sO + at);
+                uint32_t oe[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 oo = unpack2(oe[e]);
+                    const int c = 8 * i + 2 * e;
+                    oe[e] = pack2(fmaf(dtj, y[c], skip * oo.x), fmaf(dtj, y[c + 1], skip * oo.y));
+                }
+                *reinterpret_cast<uint4 *>(sm + L::STG + at) = make_uint4(oe[0], oe[1], oe[2], oe[3]);
+            }
+        }
+        wait(&b_d, ph);
+        tc::fence_after();
+        {  // dq and u: token i = row, key channels WN qc ..
+            const float er = G.er[row];
+            float us = 0.f;
+#pragma unroll
+            for (int hf = 0; hf < WN / 16; ++hf) {
+                float t[16];
+                ld16(tl + cX + WN * qc + 16 * hf, t);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(sm + L::Q + piece(kCT, row, WN / 8 * qc + 2 * hf + i));
+                    const uint32_t qe[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 qq = unpack2(qe[e]);
+                        const int c = 8 * i + 2 * e;
+                        us = fmaf(qq.x, t[c], fmaf(qq.y, t[c + 1], us));
+                        dq[16 * hf + c] = fmaf(er, t[c], dq[16 * hf + c]);
+                        dq[16 * hf + c + 1] = fmaf(er, t[c + 1], dq[16 * hf + c + 1]);
+                    }
+                }
+            }
+            us *= er;
+            up[qc][row] = x == 0 ? us : up[qc][row] + us;
+        }
+        handoff();
+        if (aborted) break;
+        if (tid == 0 && !tail) {
+            tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
+            tc::bulk_commit();
+        }
+        if (tail) {
+            bf16 *dv = static_cast<bf16 *>(a.dv) + grow * f.ldv + (size_t)h * P + 64 * x;
+            for (int i = tid; i < len * 8; i += kNT)
+                *reinterpret_cast<uint4 *>(dv + (size_t)(i / 8) * f.ldv + 8 * (i % 8)) =
+                    *reinterpret_cast<const uint4 *>(sm + L::STG + piece(kCT, i / 8, i % 8));
+        }
+        if (x == NX - 1 && warp == 3) {
+            // dla_t = sum_{i >= t} (u_i + rowsum_i - dt_i colsum_i) + sum_{j < t} dt_j r_j + e^{L_end} <E, S>,
+            // ddt_t = r_t + colsum_t + the diagonal: four tokens a lane
+            float xs[4], ys[4], rr[4], cc[4], sx = 0.f, sy = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                const float row_s = (rowp[0][t] + rowp[1][t]) + (rowp[2][t] + rowp[3][t]);
+                cc[e] = (colp[0][t] + colp[1][t]) + (colp[2][t] + colp[3][t]);
+                rr[e] = (rp[0][t] + rp[1][t]) + (rp[2][t] + rp[3][t]);
+                xs[e] = (up[0][t] + up[1][t]) + (up[2][t] + up[3][t]) + row_s - G.dt[t] * cc[e];
+                ys[e] = G.dt[t] * rr[e];
+                sx += xs[e];
+                sy += ys[e];
+            }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float px = __shfl_down_sync(0xffffffffu, sx, m), py = __shfl_up_sync(0xffffffffu, sy, m);
+                if (lane + m < 32) sx += px;
+                if (lane >= m) sy += py;
+            }
+            const float eall = warp_sum(lane < 16 ? red[lane] : 0.f) * G.gamma;
+            const float dall = warp_sum(lane < 16 ? red[16 + lane] : 0.f);
+            if (lane == 0 && a.dskip_part) a.dskip_part[slot * f.H + h] = dall;
+            float after = __shfl_down_sync(0xffffffffu, sx, 1), before = __shfl_up_sync(0xffffffffu, sy, 1);
+            if (lane == 31) after = 0.f;
+            if (lane == 0) before = 0.f;
+            float run[4];
+            run[3] = after + xs[3];
+            run[2] = run[3] + xs[2];
+            run[1] = run[2] + xs[1];
+            run[0] = run[1] + xs[0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                if (t < len) {
+                    const size_t r = (grow + t) * f.H + h;
+                    static_cast<bf16 *>(a.dla)[r] = __float2bfloat16_rn(run[e] + before + eall);
+                    static_cast<bf16 *>(a.ddt)[r] = __float2bfloat16_rn(rr[e] + cc[e] + cd[t]);
+                }
+                before += ys[e];
+            }
+        }
+    }
+
+    // ---- dq += Z k, dk += Z^T q, and out
+    if (!aborted && nu > 0) wait(&b_e, (nu - 1) & 1);
+    if (!aborted) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4 *>(sm + L::ST0 + piece(kCT, row, 4 * qc + i)) =
+                make_uint4(pack2(Z[8 * i], Z[8 * i + 1]), pack2(Z[8 * i + 2], Z[8 * i + 3]), pack2(Z[8 * i + 4], Z[8 * i + 5]),
+                           pack2(Z[8 * i + 6], Z[8 * i + 7]));
+    }
+    handoff();
+    if (!aborted) {
+        if (tid == 0) {
+            mma_tiles<true, false>(tm + cDK, sm + L::ST0, kCT, sm + L::Q, kCT, kCT / 16, idZk, nu > 0);
+            mma_tiles<false, false>(tm + cX, sm + L::ST0, kCT, sm + L::K, kCT, kCT / 16, idZq, false);
+            tc::commit(&b_z);
+        }
+        wait(&b_z, 1);
+        tc::fence_after();
+        const size_t rows = f.cu ? (size_t)f.T : (size_t)f.B * f.T;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float t[WN];
+            ldw<WN>(tl + (which ? cDK : cX) + WN * qc, t);
+            tc::wait_ld();
+            if (!which)
+#pragma unroll
+                for (int i = 0; i < WN; ++i) t[i] += dq[i];
+            if (row < len) {
+                if (a.splits == 1) {
+                    bf16 *dst = which ? static_cast<bf16 *>(a.dk) + (grow + row) * f.ldk + (size_t)g * N + WN * qc
+                                      : static_cast<bf16 *>(a.dq) + (grow + row) * f.ldq + (size_t)g * N + WN * qc;
+#pragma unroll
+                    for (int i = 0; i < WN; i += 8)
+                        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(pack2(t[i], t[i + 1]), pack2(t[i + 2], t[i + 3]),
+                                                                         pack2(t[i + 4], t[i + 5]), pack2(t[i + 6], t[i + 7]));
+                } else {
+                    float *dst = a.dqk_part + (((size_t)(which * a.splits + sp) * rows + grow + row) * f.G + g) * N + WN * qc;
+#pragma unroll
+                    for (int i = 0; i < WN; i += 4)
+                        *reinterpret_cast<float4 *>(dst + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
+                }
+            }
+        }
+    }
+    if (tid == 0) {  // nothing is left in flight
+        if (aborted) {
+            tc::commit(&b_z);
+            (void)tc::mbar_wait(&b_z, 1);
+        }
+        for (int s = 0; s < 2; ++s)
+            if (nl[s]) (void)tc::mbar_wait(&ld[s], (nl[s] - 1) & 1);
+        tc::bulk_wait();
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+template <int N, int P>
+cudaError_t bwd_np(const ScanBwdArgs &a, cudaStream_t s) {
+    const ScanArgs &f = a.f;
+    BwdMaps m;
+    const int MB = f.cu ? 1 : f.B;
+    if (!scan_tile_map(&m.q, f.q, f.ldq, MB, f.T, f.G, N) || !scan_tile_map(&m.k, f.k, f.ldk, MB, f.T, f.G, N) ||
+        !scan_tile_map(&m.v, f.v, f.ldv, MB, f.T, f.H, P) || !scan_tile_map(&m.dv, a.dv, f.ldv, MB, f.T, f.H, P) ||
+        !scan_tile_map(&m.dO, a.dO, (long long)f.H * P, MB, f.T, f.H, P))
+        return cudaErrorInvalidValue;
+    auto kernel = bwd_kernel<N, P>;
+    constexpr int bytes = BwdTcSmem<N>::BYTES;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(slot_count(f.cu, f.B, f.T, kCT) * f.G * a.splits), kNT, bytes, s>>>(a, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_scan_bwd_tc(const ScanBwdArgs &a, int dk, int dv, cudaStream_t s) {
+    cudaError_t e = launch_scan_grads_tc(a, dk, dv, s);
+    if (e != cudaSuccess) return e;
+    if (dk == 128) e = dv == 128 ? bwd_np<128, 128>(a, s) : bwd_np<128, 64>(a, s);
+    else e = dv == 128 ? bwd_np<64, 128>(a, s) : bwd_np<64, 64>(a, s);
+    return e != cudaSuccess ? e : launch_grad_sums(a, dk, true, kCT, s);
+}
+
+}  // namespace ssm
+}  // namespace gdn2

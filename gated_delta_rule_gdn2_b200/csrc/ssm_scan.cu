@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
 }
 
 // dq, dk from the splits' sums, added in order; one row a block.
+template <typename T>
 __global__ void qk_reduce_kernel(ScanBwdArgs a, int N) {
     const ScanArgs &f = a.f;
     const long long row = blockIdx.x;
@@ -626,7 +627,7 @@ __global__ void qk_reduce_kernel(ScanBwdArgs a, int N) {
             const int mid = (lo + hi + 1) >> 1;
             if (f.cu[mid] <= row) lo = mid; else hi = mid - 1;
         }
-        const Seq s = seq_of(f.cu, lo, f.T, kC);
+        const Seq s = seq_of(f.cu, lo, f.T, 1);
         if (!s.ok || row < s.row0 || row >= s.row0 + s.len) return;
     }
     for (int c = threadIdx.x; c < 2 * (int)W; c += blockDim.x) {
@@ -634,11 +635,9 @@ __global__ void qk_reduce_kernel(ScanBwdArgs a, int N) {
         const float *p = a.dqk_part + ((size_t)which * a.splits * rows + row) * W + x;
         float s = 0.f;
         for (int i = 0; i < a.splits; ++i) s += p[(size_t)i * rows * W];
-        (which ? static_cast<float *>(a.dk) + row * f.ldk : static_cast<float *>(a.dq) + row * f.ldq)[x] = s;
+        (which ? static_cast<T *>(a.dk) + row * f.ldk : static_cast<T *>(a.dq) + row * f.ldq)[x] = from_f32<T>(s);
     }
 }
-
-}  // namespace
 
 // dskip[h] = the sum over the slots, by one block a head.
 __global__ void dskip_reduce_kernel(const float *part, long long slots, int H, float *dskip) {
@@ -654,6 +653,8 @@ __global__ void dskip_reduce_kernel(const float *part, long long slots, int H, f
     }
     if (threadIdx.x == 0) dskip[h] = red[0];
 }
+
+}  // namespace
 
 cudaError_t launch_scan_fwd_f32(const ScanArgs &a, int dk, int dv, cudaStream_t s) {
     RecArgs r{static_cast<const float *>(a.q), static_cast<const float *>(a.k), static_cast<const float *>(a.v),
@@ -686,14 +687,20 @@ cudaError_t launch_scan_bwd_f32(const ScanBwdArgs &a, int dk, int dv, cudaStream
     using I128 = std::integral_constant<int, 128>;
     if (dk == 128) e = dv == 128 ? go(I128{}, I128{}) : go(I128{}, I64{});
     else e = dv == 128 ? go(I64{}, I128{}) : go(I64{}, I64{});
-    if (e != cudaSuccess) return e;
+    return e != cudaSuccess ? e : launch_grad_sums(a, dk, false, kC, s);
+}
+
+cudaError_t launch_grad_sums(const ScanBwdArgs &a, int dk, bool bf16, int chunk, cudaStream_t s) {
+    const ScanArgs &f = a.f;
+    cudaError_t e = cudaSuccess;
     if (a.splits > 1) {
-        const long long rows = f.cu ? (long long)f.T : (long long)f.B * f.T;
-        qk_reduce_kernel<<<(unsigned)rows, 256, 0, s>>>(a, dk);
+        const unsigned rows = (unsigned)(f.cu ? (long long)f.T : (long long)f.B * f.T);
+        if (bf16) qk_reduce_kernel<__nv_bfloat16><<<rows, 256, 0, s>>>(a, dk);
+        else qk_reduce_kernel<float><<<rows, 256, 0, s>>>(a, dk);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (a.dskip) {
-        dskip_reduce_kernel<<<f.H, 256, 0, s>>>(a.dskip_part, slots, f.H, a.dskip);
+        dskip_reduce_kernel<<<f.H, 256, 0, s>>>(a.dskip_part, slot_count(f.cu, f.B, f.T, chunk), f.H, a.dskip);
         e = cudaGetLastError();
     }
     return e;

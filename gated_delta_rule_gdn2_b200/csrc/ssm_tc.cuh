@@ -1,0 +1,200 @@
+// Pieces shared by the tensor-core kernels of the selective state space scan:
+// tensor maps of strided token tensors, tile addressing, 32-lane tensor-memory
+// accesses, the product whose left operand lies in tensor memory, and the
+// decay factors of a chunk.
+//
+// Tiles are [rows][64] bf16 blocks of 128-byte rows, their 16-byte pieces
+// permuted by row mod 8 (the 128-byte swizzle): a [R][D] tile is D / 64 such
+// blocks of R rows, one after the other.
+#pragma once
+
+#include "gdn2.h"
+#include "ssm.h"
+#include "tc.cuh"
+#include "tc_tiles.cuh"
+#include "tma_host.h"
+
+namespace gdn2 {
+namespace ssm {
+
+constexpr int kCT = 128;   // tokens of a chunk of the tensor-core kernels
+constexpr int kNT = 512;   // their threads: four warps per tensor-memory sub-partition
+constexpr float kLogMin = -104.f;  // e^{-104} is 0 in fp32: a stronger decay changes nothing
+
+// [B][T] rows, ld elements apart, of `heads` heads of D channels, in boxes of
+// 128 tokens x 64 channels of one head: coordinates (0, token, channel / 64, head, batch).
+inline bool scan_tile_map(CUtensorMap *m, const void *base, long long ld, int B, int T, int heads, int D) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[5] = {64, (cuuint64_t)T, (cuuint64_t)(D / 64), (cuuint64_t)heads, (cuuint64_t)B};
+    const cuuint64_t strides[4] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)D * 2, (cuuint64_t)T * (cuuint64_t)ld * 2};
+    const cuuint32_t box[5] = {64, (cuuint32_t)kCT, 1, 1, 1};
+    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef __nv_bfloat16 bf16;
+
+__device__ __forceinline__ void tma_store_5d(const void *map, const void *src, int y, int z, int w, int v) {
+    asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];\n" ::"l"(map),
+                 "r"(0), "r"(y), "r"(z), "r"(w), "r"(v), "r"(tc::smem_addr(src))
+                 : "memory");
+}
+
+// D (+)= A B with A [128][K] bf16 in tensor memory (two values a column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0));
+}
+
+__device__ __forceinline__ void ld16(uint32_t t, float (&v)[16]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t));
+}
+__device__ __forceinline__ void st16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+__device__ __forceinline__ void ld8(uint32_t t, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t));
+}
+__device__ __forceinline__ void st8(uint32_t t, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(t), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+// 16 or 32 consecutive columns of this thread's lane
+template <int W>
+__device__ __forceinline__ void ldw(uint32_t t, float (&v)[W]) {
+    if constexpr (W == 16) ld16(t, v);
+    else tc::ld_32x32b_x32(t, v);
+}
+template <int W>
+__device__ __forceinline__ void stw(uint32_t t, const float (&v)[W]) {
+    if constexpr (W == 16) st16(t, reinterpret_cast<const uint32_t(&)[16]>(v));
+    else tc::st_32x32b_x32(t, v);
+}
+
+// Byte offset of piece `p8` (8 channels) of row r in a [R][.] tile.
+__device__ __forceinline__ uint32_t piece(int R, int r, int p8) {
+    return (uint32_t)((p8 >> 3) * (R * 128) + r * 128 + (((p8 & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u)); }
+
+// W consecutive fp32 values of row r from column c0 on, rounded to bf16, into a tile.
+template <int W>
+__device__ __forceinline__ void put_row(unsigned char *tile, int R, int r, int c0, const float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i)
+        *reinterpret_cast<uint4 *>(tile + piece(R, r, c0 / 8 + i)) =
+            make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]), pack2(v[8 * i + 4], v[8 * i + 5]),
+                       pack2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// Decay factors of a chunk, by blocks of 32 tokens (one warp each): exponents
+// of products across blocks are sums of terms <= 0, so none overflows and none
+// is a difference of long sums.
+//   l    log decay from the block's start through the token
+//   cf   e^{log decay from behind the token to the block's end} (FWD: times dt)
+//   er   e^{log decay from the chunk's start through the token}
+//   wt   e^{log decay from behind the token to the chunk's end} (FWD: times dt)
+//   dt   the step size
+struct alignas(16) Gates {  // (read in 16-byte pieces, two side by side)
+    float l[kCT], cf[kCT], er[kCT], wt[kCT], dt[kCT];
+    float bs[4];    // the blocks' log decays
+    float gamma;    // the chunk's decay
+    float total;    // its log
+};
+// Formed by four whole warps (t = 0..127 within them), with a named barrier
+// between the blocks' sums and what crosses blocks; `carry`: a log decay to add to wt's exponent.
+__device__ __forceinline__ void form_gates(Gates &g, float la, float dt, int t, int bar, float carry) {
+    const int lane = t & 31, w = t >> 5;
+    float up = la, dn = la;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, up, m), z = __shfl_down_sync(0xffffffffu, dn, m);
+        if (lane >= m) up += y;
+        if (lane + m < 32) dn += z;
+    }
+    const float behind = __shfl_down_sync(0xffffffffu, dn, 1), s = lane < 31 ? behind : 0.f;
+    g.l[t] = up;
+    g.cf[t] = __expf(s) * dt;
+    g.dt[t] = dt;
+    if (lane == 31) g.bs[w] = up;
+    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
+    const float b0 = g.bs[0], b1 = g.bs[1], b2 = g.bs[2], b3 = g.bs[3];
+    const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
+    const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
+    g.er[t] = __expf(pre + up);
+    g.wt[t] = __expf(s + post + carry) * dt;
+    if (t == 0) {
+        const float all = b0 + b1 + b2 + b3;
+        g.gamma = __expf(all);
+        g.total = all;
+    }
+}
+// log decay of the blocks strictly between block a and block b > a
+__device__ __forceinline__ float between(const Gates &g, int a, int b) {
+    float s = 0.f;
+    if (a < 1 && b > 1) s += g.bs[1];
+    if (a < 2 && b > 2) s += g.bs[2];
+    return s;
+}
+
+// Rows [len, 128) of a [128][64 nblk] tile set to zero (the last chunk of a
+// packed sequence, whose box reaches into the next one).
+__device__ __forceinline__ void zero_tail(unsigned char *tile, int nblk, int len, int tid, int nt) {
+    const int n = (kCT - len) * 8;
+    for (int i = tid; i < n * nblk; i += nt) {
+        const int blk = i / n, x = i % n;
+        *reinterpret_cast<uint4 *>(tile + blk * (kCT * 128) + (len + x / 8) * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Rows of a [128][64 w] tile scaled by f[row], in two bf16 parts whose sum
+// carries 16 bits: the parts of the first go in place, of the rest to `lo`.
+// Rows from len on become zero whatever they hold.
+template <int D>
+__device__ __forceinline__ void scale_hi_lo(unsigned char *hi, unsigned char *lo, const float *f, int len, int tid) {
+    constexpr int PPR = D / 8;  // pieces a row
+#pragma unroll
+    for (int i = 0; i < kCT * PPR / kNT; ++i) {
+        // eight consecutive lanes take the eight pieces of one 128-byte row
+        const int id = tid + i * kNT, blk = id / (kCT * 8), r = (id / 8) % kCT;
+        const uint32_t at = (uint32_t)(blk * (kCT * 128) + r * 128 + (id % 8) * 16);
+        uint4 x = *reinterpret_cast<const uint4 *>(hi + at), y;
+        const float w = f[r];
+        uint32_t *xe = reinterpret_cast<uint32_t *>(&x), *ye = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = unpack2(xe[e]);
+            const float a = v.x * w, b = v.y * w;
+            const uint32_t h = pack2(a, b);
+            const float2 hf = unpack2(h);
+            xe[e] = r < len ? h : 0u;
+            ye[e] = r < len ? pack2(a - hf.x, b - hf.y) : 0u;
+        }
+        *reinterpret_cast<uint4 *>(hi + at) = x;
+        *reinterpret_cast<uint4 *>(lo + at) = y;
+    }
+}
+
+}  // namespace ssm
+}  // namespace gdn2

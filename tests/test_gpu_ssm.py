@@ -17,7 +17,7 @@ pytestmark = pytest.mark.gpu
 F64 = torch.float64
 NAMES = ("q", "k", "v", "la", "dt", "skip", "S0")
 GRADS = ("dq", "dk", "dv", "dlog_alpha", "ddt")
-SCAN = ["fp32"]  # element types of the scan
+SCAN = ["fp32", "bf16"]  # element types of the scan
 TD = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
 
