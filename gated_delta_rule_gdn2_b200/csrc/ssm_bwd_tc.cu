@@ -50,17 +50,17 @@ __device__ __forceinline__ void form_bwd_gates(BwdGates &g, float la, float dt, 
     }
     const float behind = __shfl_down_sync(0xffffffffu, dn, 1), s = lane < 31 ? behind : 0.f;
     g.l[t] = up;
-    g.lf[t] = __expf(up);
-    g.cf[t] = __expf(s);
+    g.lf[t] = exp_ftz(up);
+    g.cf[t] = exp_ftz(s);
     g.dt[t] = dt;
     if (lane == 31) g.bs[w] = up;
     asm volatile("bar.sync 1, 128;\n" ::: "memory");
     const float b0 = g.bs[0], b1 = g.bs[1], b2 = g.bs[2], b3 = g.bs[3];
     const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
     const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
-    g.er[t] = __expf(pre + up);
-    g.wt[t] = __expf(s + post);
-    if (t == 0) g.gamma = __expf(b0 + b1 + b2 + b3);
+    g.er[t] = exp_ftz(pre + up);
+    g.wt[t] = exp_ftz(s + post);
+    if (t == 0) g.gamma = exp_ftz(b0 + b1 + b2 + b3);
 }
 
 // Sums over the 32 lanes of 16 values a lane: lanes 2 c and 2 c + 1 end with
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     tc::fence_after();
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
 
-    int nl[2] = {0, 0};
+    int nl = 0;
     auto load = [&](int u) {
         const int s = u & 1, h = h_lo + u / NX, x = u % NX;
         unsigned char *st = sm + L::ST0 + s * L::STAGE;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         const size_t img = ((size_t)slot * f.H + h) * (N * P * 2) + (size_t)x * L::SB;
         tc::bulk_load(st + 2 * L::VB, static_cast<const unsigned char *>(a.grads) + img, L::SB, &ld[s]);
         tc::bulk_load(st + 2 * L::VB + L::SB, static_cast<const unsigned char *>(f.states) + img, L::SB, &ld[s]);
-        ++nl[s];
+        ++nl;
     };
     bool bad = false, aborted = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         // ---- X: token j = row, tokens i = 32 qc ..
         if (qc >= p) {
             const float lj = G.l[row];
-            const float fj = qc > p ? G.cf[row] * __expf(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]) : 0.f;
+            const float fj = qc > p ? G.cf[row] * exp_ftz(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]) : 0.f;
             float col = 0.f;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                         d1 = lf.y * fj;
                     } else {
                         const float2 l2 = *reinterpret_cast<const float2 *>(&G.l[32 * qc + i0]);
-                        d0 = i0 >= lane ? __expf(l2.x - lj) : 0.f;
-                        d1 = i0 + 1 >= lane ? __expf(l2.y - lj) : 0.f;
+                        d0 = i0 >= lane ? exp_ftz(l2.x - lj) : 0.f;
+                        d1 = i0 + 1 >= lane ? exp_ftz(l2.y - lj) : 0.f;
                     }
                     const float x0 = X[i] * d0, x1 = X[i + 1] * d1;
                     Z[i0] = fmaf(x0, dtj, Z[i0]);
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             tc::commit(&b_z);
             (void)tc::mbar_wait(&b_z, 1);
         }
-        for (int s = 0; s < 2; ++s)
-            if (nl[s]) (void)tc::mbar_wait(&ld[s], (nl[s] - 1) & 1);
+        if (nl > 0) (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
+        if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
         tc::bulk_wait();
     }
     tc::fence_before();

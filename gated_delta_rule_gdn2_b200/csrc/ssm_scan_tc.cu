@@ -5,7 +5,8 @@
 // A CTA of 16 warps takes one (sequence, head) -- or one part of it -- and
 // walks its chunks of 128 tokens with the fp32 state S [dk][dv] in tensor
 // memory.  In a chunk, with L_i the log decay from its start through token i,
-//     o_i = e^{L_i} S^T q_i + sum_{j <= i} (q_i . k_j) e^{L_i - L_j} dt_j v_j + skip v_i,
+//     o_i = e^{L_i} S^T q_i + sum_{j <= i} M_ij v_j,
+//     M_ij = (q_i . k_j) e^{L_i - L_j} dt_j (+ skip where i = j),
 //     S  <- e^{L_end} S + sum_j e^{L_end - L_j} dt_j k_j v_j^T,
 // as four products: G = q k^T; q S (S rounded to bf16); M v, with M = G masked,
 // decayed and rounded to bf16, written back to tensor memory as the left
@@ -33,7 +34,7 @@ namespace {
 using tct::mma_tiles;
 
 struct Maps {
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v;
 };
 
 // The state (or gradient) that reaches part `part`, W columns of row r.
@@ -65,32 +66,55 @@ __device__ __forceinline__ void start_state(const float *first, const float *par
 __device__ __forceinline__ float token(const void *p, size_t i) { return __bfloat162float(static_cast<const bf16 *>(p)[i]); }
 
 // ---------------------------------------------------------------------------
-// Forward
+// Forward.  Four roles: warp 16 issues the copies and the products, warp 17
+// forms the decay factors up to four chunks ahead, and the other sixteen work
+// in two groups that meet only through mbarriers, so that the state-free half
+// of chunk m + 1 runs beside the state's half of chunk m:
+//   A (warps 0..7)   the two parts of the scaled k in shared memory; M from G
+//   B (warps 8..15)  q S scaled by e^L in place (M v is added to it); the
+//                    state's bf16 copy and its decay; o
+// A thread of either group owns a row (token or key channel) of tensor memory
+// and half of its columns.
+
+constexpr int kFwdThreads = 18 * 32, kRing = 4;
 
 template <int N, int P>
 struct FwdSmem {
     static constexpr int QB = kCT * N * 2, VB = kCT * P * 2;
-    // lo: the second part of the scaled k, and later the o tile.  (At N = 64 the
-    // state's product reads 128 rows of its left operand; the upper 64 are
-    // whatever block follows, and go to rows of S that nothing reads.)
-    static constexpr int LO = 0, K0 = (QB > VB ? QB : VB), K1 = K0 + QB, Q = K1 + QB, V = Q + QB, S16 = V + VB,
-                         G = S16 + N * P * 2, END = G + 2 * (int)sizeof(Gates);
+    // (At N = 64 the state's product reads 128 rows of its left operand; the
+    // upper 64 are whatever block follows, and go to rows of S that nothing reads.)
+    static constexpr int LO = 0, K0 = QB, K1 = K0 + QB, Q = K1 + QB, V = Q + QB, S16 = V + VB, G = S16 + N * P * 2,
+                         END = G + kRing * (int)sizeof(Gates);
     static constexpr int BYTES = END + 1024;
 };
 
+// 32 bytes of a row (16 values as bf16) to global memory.
+__device__ __forceinline__ void store32(bf16 *dst, const uint32_t (&u)[8], bool wide) {
+    if (wide) {  // whole sectors
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+}
+
 template <int N, int P>
-__global__ void __launch_bounds__(kNT, 1) fwd_kernel(ScanArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const __grid_constant__ Maps maps) {
     using L = FwdSmem<N, P>;
-    constexpr int W = P / 4;  // columns of a thread in a P-column row
+    constexpr int HP = P / 2;  // columns of a thread in a P-column row
     constexpr uint32_t cS = 0, cG = 128, cY = 256, cM = 384;  // tensor-memory columns
     constexpr uint32_t idG = tc::idesc_bf16(128, 128, false, false), idY = tc::idesc_bf16(128, P, false, true),
                        idS = tc::idesc_bf16(128, P, true, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t ld_q, ld_k[2], ld_v, b_g, b_y1, b_s, b_y2, b_fin;
+    // tiles landed; products done; hand-overs of the groups (one arrival a warp)
+    __shared__ uint64_t ld_q, ld_k[2], ld_v, d_g, d_yi, d_s, d_y, r_hl, r_m, r_ys, r_st, r_o, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, qc = warp >> 2, row = 32 * p + lane;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, half = (warp >> 2) & 1, row = 32 * p + lane;
     const int part = blockIdx.x % a.parts, bh = blockIdx.x / a.parts, b = bh / a.H, h = bh % a.H, g = h / (a.H / a.G);
     const Seq sq = seq_of(a.cu, b, a.T, kCT);
     if (!sq.ok) {
@@ -100,249 +124,300 @@ __global__ void __launch_bounds__(kNT, 1) fwd_kernel(ScanArgs a, const __grid_co
     const int cpp = (sq.nchunks + a.parts - 1) / a.parts, c_lo = min(part * cpp, sq.nchunks),
               n_chunks = min((part + 1) * cpp, sq.nchunks) - c_lo;
     const bool last_part = part == a.parts - 1;
-    const float skip = a.skip ? a.skip[h] : 0.f;
     const int mb = a.cu ? 0 : b, mt = (a.cu ? (int)sq.row0 : 0) + c_lo * kCT;  // coordinates of the part's first row
 
-    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == 16) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        uint64_t *bars[] = {&ld_q, &ld_k[0], &ld_k[1], &ld_v, &b_g, &b_y1, &b_s, &b_y2, &b_fin};
-        for (uint64_t *x : bars) tc::mbar_init(x, 1);
+        uint64_t *one[] = {&ld_q, &ld_k[0], &ld_k[1], &ld_v, &d_g, &d_yi, &d_s, &d_y, &d_fin};
+        for (uint64_t *x : one) tc::mbar_init(x, 1);
+        uint64_t *eight[] = {&r_hl, &r_m, &r_ys, &r_st, &r_o};
+        for (uint64_t *x : eight) tc::mbar_init(x, 8);
+        for (int i = 0; i < kRing; ++i) {
+            tc::mbar_init(&r_gate[i], 1);
+            tc::mbar_init(&r_gfree[i], 16);
+        }
         tc::fence_mbar_init();
+        dead = 0;
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
 
-    int nq = 0, nk[2] = {0, 0}, nv = 0;  // (thread 0) loads issued
-    auto load_q = [&](int m) {
-        tc::mbar_expect_tx(&ld_q, L::QB);
-        for (int x = 0; x < N / 64; ++x) tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt + m * kCT, x, g, mb, &ld_q);
-        ++nq;
-    };
-    auto load_k = [&](int m) {
-        const int s = m & 1;
-        tc::mbar_expect_tx(&ld_k[s], L::QB);
-        for (int x = 0; x < N / 64; ++x)
-            tc::tma_load_5d(sm + (s ? L::K1 : L::K0) + x * kCT * 128, &maps.k, 0, mt + m * kCT, x, g, mb, &ld_k[s]);
-        ++nk[s];
-    };
-    auto load_v = [&](int m) {
-        tc::mbar_expect_tx(&ld_v, L::VB);
-        for (int x = 0; x < P / 64; ++x) tc::tma_load_5d(sm + L::V + x * kCT * 128, &maps.v, 0, mt + m * kCT, x, h, mb, &ld_v);
-        ++nv;
-    };
-    bool bad = false, aborted = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!tc::mbar_wait(bar, parity)) {
-            bad = true;
-            record_status(a.status, GDN2_ERR_TIMEOUT);
-        }
-    };
-    // what the threads wrote becomes visible to the tensor cores and copies; a
-    // wait that ran out in one thread ends the walk for all of them together
-    auto handoff = [&]() {
+    // a bounded wait by a whole warp, with one answer for all its lanes
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &dead)) != 0; };
+    // what this warp wrote, and read, handed over
+    auto give = [&](uint64_t *bar) {
         tc::fence_async_smem();
         tc::fence_before();
-        aborted = __syncthreads_or(bad);
-        tc::fence_after();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
     };
-    if (tid == 0 && n_chunks > 0) {
-        load_q(0);
-        load_k(0);
-        load_v(0);
-        if (n_chunks > 1) load_k(1);
-    }
-    // the last four warps form the decay factors, one chunk ahead, from values loaded two ahead
-    float g_la = 0.f, g_dt = 0.f;
-    const int gt = tid - (kNT - kCT);
-    auto load_gates = [&](int m) {
-        const int t = (c_lo + m) * kCT + gt;
-        g_la = g_dt = 0.f;
-        if (m < n_chunks && t < sq.len) {
-            const size_t r = (size_t)(sq.row0 + t) * a.H + h;
-            g_la = fmaxf(token(a.la, r), kLogMin);
-            g_dt = token(a.dt, r);
-        }
-    };
-    if (gt >= 0) {
-        load_gates(0);
-        form_gates(gates[0], g_la, g_dt, gt, 1, 0.f);
-        load_gates(1);
-    }
-    float S[W];
-    start_state<N, P, W, false>(a.S0, a.part_state, a.part_decay, a.parts, part, bh, row, W * qc, S);
-    if (n_chunks > 0 && row < N) put_row<W>(sm + L::S16, N, row, W * qc, S);
-    __syncthreads();
-    if (n_chunks > 0) {
-        const float gm = gates[0].gamma;
-        float t[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) t[i] = S[i] * gm;
-        stw<W>(tl + cS + W * qc, t);
-        tc::wait_st();
-    }
-    handoff();
+    // chunk m's parity on a barrier that completes once a chunk, or once in R chunks
+    auto par = [](int m, int R) { return (uint32_t)(m / R) & 1u; };
 
-    for (int m = 0; m < n_chunks; ++m) {
-        const int s = m & 1, len = min(kCT, sq.len - (c_lo + m) * kCT);
-        const uint32_t ph = m & 1, ph2 = (m >> 1) & 1;
-        const Gates &G = gates[s];
-        unsigned char *K = sm + (s ? L::K1 : L::K0);
-        if (tid == 0) {
-            tc::bulk_wait_read();  // the o tile of the chunk before
-            wait(&ld_q, ph);
-            wait(&ld_k[s], ph2);
-            mma_tiles<true, true>(tm + cG, sm + L::Q, kCT, K, kCT, N / 16, idG, false);
-            tc::commit(&b_g);
-            mma_tiles<true, false>(tm + cY, sm + L::Q, kCT, sm + L::S16, N, N / 16, idY, false);
-            tc::commit(&b_y1);
-            if (a.states) {  // the state at the chunk's start, as it lies here
-                tc::bulk_store(static_cast<unsigned char *>(a.states) +
-                                   ((size_t)(sq.slot + c_lo + m) * a.H + h) * (N * P * 2),
-                               sm + L::S16, N * P * 2);
-                tc::bulk_commit();
-            }
-        }
-        wait(&b_g, ph);
-        tc::fence_after();
-        scale_hi_lo<N>(K, sm + L::LO, G.wt, len, tid);
-        if (a.cu && len < kCT) {
-            wait(&ld_v, ph);
-            zero_tail(sm + L::V, P / 64, len, tid, kNT);
-        }
-        handoff();
-        if (aborted) break;
-        if (tid == 0) {
-            wait(&ld_v, ph);
-            mma_tiles<false, false>(tm + cS, K, kCT, sm + L::V, kCT, kCT / 16, idS, true);
-            mma_tiles<false, false>(tm + cS, sm + L::LO, kCT, sm + L::V, kCT, kCT / 16, idS, true);
-            tc::commit(&b_s);
-        }
-        // M = G masked and decayed: this thread's row i = row, columns 32 qc ..
-        {
-            uint32_t u[16];
-            if (qc > p) {
+    if (warp == 16) {
+        if (n_chunks > 0) {
+            int nq = 0, nk = 0, nv = 0;  // loads issued
+            auto load_q = [&](int m) {
+                ++nq;
+                if (!elect()) return;
+                tc::mbar_expect_tx(&ld_q, L::QB);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = 0u;
-            } else {
-                float x[32];
-                tc::ld_32x32b_x32(tl + cG + 32 * qc, x);
-                const float li = G.l[row];
-                const float f = qc < p ? __expf(li + between(G, qc, p)) : 0.f;
-                tc::wait_ld();
+                for (int x = 0; x < N / 64; ++x) tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt + m * kCT, x, g, mb, &ld_q);
+            };
+            auto load_k = [&](int m) {
+                ++nk;
+                if (!elect()) return;
+                uint64_t *bar = &ld_k[m & 1];
+                unsigned char *dst = sm + L::K0 + (m & 1) * L::QB;
+                tc::mbar_expect_tx(bar, L::QB);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    float c[4];
-                    if (qc < p) {
-                        const float4 cf = *reinterpret_cast<const float4 *>(&G.cf[32 * qc + i]);
-                        c[0] = f * cf.x; c[1] = f * cf.y; c[2] = f * cf.z; c[3] = f * cf.w;
-                    } else {
-                        const float4 l4 = *reinterpret_cast<const float4 *>(&G.l[32 * qc + i]);
-                        const float4 d4 = *reinterpret_cast<const float4 *>(&G.dt[32 * qc + i]);
-                        c[0] = __expf(li - l4.x) * d4.x; c[1] = __expf(li - l4.y) * d4.y;
-                        c[2] = __expf(li - l4.z) * d4.z; c[3] = __expf(li - l4.w) * d4.w;
+                for (int x = 0; x < N / 64; ++x) tc::tma_load_5d(dst + x * kCT * 128, &maps.k, 0, mt + m * kCT, x, g, mb, bar);
+            };
+            auto load_v = [&](int m) {
+                ++nv;
+                if (!elect()) return;
+                tc::mbar_expect_tx(&ld_v, L::VB);
+#pragma unroll
+                for (int x = 0; x < P / 64; ++x) tc::tma_load_5d(sm + L::V + x * kCT * 128, &maps.v, 0, mt + m * kCT, x, h, mb, &ld_v);
+            };
+            auto product_G = [&](int m) {
+                if (!elect()) return;
+                mma_tiles<true, true>(tm + cG, sm + L::Q, kCT, sm + L::K0 + (m & 1) * L::QB, kCT, N / 16, idG, false);
+                tc::commit(&d_g);
+            };
+            load_q(0);
+            load_k(0);
+            load_v(0);
+            if (n_chunks > 1) load_k(1);
+            bool ok = wait(&ld_q, 0) && wait(&ld_k[0], 0);
+            if (ok) product_G(0);
+            int m = 0;
+            for (; ok && m < n_chunks; ++m) {
+                const uint32_t ph = m & 1;
+                const bool more = m + 1 < n_chunks;
+                if (!(ok = wait(&r_st, ph) && (m == 0 || wait(&r_o, ph ^ 1)))) break;
+                tc::fence_after();
+                if (m > 0) load_v(m);
+                if (elect()) {
+                    mma_tiles<true, false>(tm + cY, sm + L::Q, kCT, sm + L::S16, N, N / 16, idY, false);
+                    tc::commit(&d_yi);
+                    if (a.states) {  // the state at the chunk's start, as it lies here
+                        tc::bulk_store(static_cast<unsigned char *>(a.states) +
+                                           ((size_t)(sq.slot + c_lo + m) * a.H + h) * (N * P * 2),
+                                       sm + L::S16, N * P * 2);
+                        tc::bulk_commit();
                     }
+                }
+                if (!(ok = wait(&r_hl, ph) && wait(&ld_v, ph))) break;
+                tc::fence_after();
+                if (elect()) {
+                    mma_tiles<false, false>(tm + cS, sm + L::K0 + (m & 1) * L::QB, kCT, sm + L::V, kCT, kCT / 16, idS, true);
+                    mma_tiles<false, false>(tm + cS, sm + L::LO, kCT, sm + L::V, kCT, kCT / 16, idS, true);
+                    tc::bulk_wait_read();  // (the commit lets group B overwrite S16)
+                    tc::commit(&d_s);
+                }
+                if (more) {
+                    if (!(ok = wait(&d_yi, ph))) break;
+                    load_q(m + 1);
+                }
+                if (!(ok = wait(&r_m, ph) && wait(&r_ys, ph))) break;
+                tc::fence_after();
+                if (elect()) {
+                    const uint64_t v0 = tct::mnmaj(sm + L::V, kCT, 0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i + e] = qc < p || i + e <= lane ? x[i + e] * c[e] : 0.f;
-                    u[i / 2] = pack2(x[i], x[i + 1]);
-                    u[i / 2 + 1] = pack2(x[i + 2], x[i + 3]);
+                    for (int x = 0; x < kCT / 16; ++x)
+                        mma_ts(tm + cY, tm + cM + 8 * x, v0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, true);
+                    tc::commit(&d_y);
+                }
+                if (more) {
+                    if (!(ok = wait(&ld_q, ph ^ 1) && wait(&ld_k[(m + 1) & 1], par(m + 1, 2)))) break;
+                    product_G(m + 1);
+                    if (!(ok = wait(&d_s, ph))) break;
+                    if (m + 2 < n_chunks) load_k(m + 2);
                 }
             }
-            st16(tl + cM + 16 * qc, u);
+            if (elect()) {  // nothing is left in flight
+                tc::commit(&d_fin);
+                tc::bulk_wait();
+            }
+            (void)tc::mbar_wait(&d_fin, 0);
+            (void)tc::mbar_wait(&ld_q, (nq - 1) & 1);
+            (void)tc::mbar_wait(&ld_v, (nv - 1) & 1);
+            (void)tc::mbar_wait(&ld_k[0], ((nk - 1) >> 1) & 1);
+            if (nk > 1) (void)tc::mbar_wait(&ld_k[1], ((nk - 2) >> 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        for (int m = 0; m < n_chunks; ++m) {
+            if (m >= kRing && !wait(&r_gfree[m % kRing], par(m - kRing, kRing))) break;
+            form_gates_warp(gates[m % kRing], a.la, a.dt, (size_t)sq.row0 * a.H + h, a.H, (c_lo + m) * kCT, sq.len, lane);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&r_gate[m % kRing]);
+        }
+    } else if (warp < 8) {
+        const int gt = tid;  // 0 .. 255
+        const float skip = a.skip ? a.skip[h] : 0.f;
+        {  // (blocks j > i of M stay zero)
+            const uint32_t z[16] = {0};
+            for (int blk = 2 * half; blk < 2 * half + 2; ++blk)
+                if (blk > p) st16(tl + cM + 16 * blk, z);
             tc::wait_st();
         }
-        if (gt >= 0) {
-            form_gates(gates[s ^ 1], g_la, g_dt, gt, 1, 0.f);
-            load_gates(m + 2);
-        }
-        if (tid == 0) tc::bulk_wait_read();  // S16 has been read
-        handoff();
-        if (aborted) break;
-        if (tid == 0) {
-            const uint64_t dv0 = tct::mnmaj(sm + L::V, kCT, 0);
-#pragma unroll
-            for (int x = 0; x < kCT / 16; ++x)
-                mma_ts(tm + cG, tm + cM + 8 * x, dv0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, x > 0);
-            tc::commit(&b_y2);
-        }
-        wait(&b_y1, ph);
-        if (tid == 0 && m + 1 < n_chunks) load_q(m + 1);
-        // the state behind this chunk: its bf16 copy, and decayed for the next
-        wait(&b_s, ph);
-        tc::fence_after();
-        if (tid == 0 && m + 2 < n_chunks) load_k(m + 2);
-        {
-            ldw<W>(tl + cS + W * qc, S);
-            tc::wait_ld();
-            if (m + 1 < n_chunks) {
-                if (row < N) put_row<W>(sm + L::S16, N, row, W * qc, S);
-                const float gm = gates[s ^ 1].gamma;
-                float t[W];
-#pragma unroll
-                for (int i = 0; i < W; ++i) t[i] = S[i] * gm;
-                stw<W>(tl + cS + W * qc, t);
-                tc::wait_st();
+        for (int m = 0; m < n_chunks; ++m) {
+            const uint32_t ph = m & 1;
+            const int len = min(kCT, sq.len - (c_lo + m) * kCT);
+            const Gates &G = gates[m % kRing];
+            // (the second part's tile was last read by the product before)
+            if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&d_g, ph) || (m > 0 && !wait(&d_s, ph ^ 1))) break;
+            scale_hi_lo<N, 256>(sm + (m & 1 ? L::K1 : L::K0), sm + L::LO, G.wt, len, gt);
+            if (a.cu && len < kCT) {
+                if (!wait(&ld_v, ph)) break;
+                zero_tail(sm + L::V, P / 64, len, gt, 256);
             }
-        }
-        wait(&b_y2, ph);
-        tc::fence_after();
-        if (a.o) {
-            float y[W], z[W];
-            ldw<W>(tl + cY + W * qc, y);
-            ldw<W>(tl + cG + W * qc, z);
-            const float er = G.er[row];
-            tc::wait_ld();
+            give(&r_hl);
+            // M = G masked and decayed, skip on its diagonal: row i = row,
+            // columns 64 half ..  (Column factors are fetched whole before the
+            // tile's values: a shared load takes hundreds of cycles while the
+            // products stream their operands.)
+            tc::fence_after();
+            if (m > 0 && !wait(&d_y, ph ^ 1)) break;  // the M before has been read
+            tc::fence_after();
+            const float li = G.l[row];
+#pragma unroll 1
+            for (int c0 = 64 * half; c0 < 64 * half + 64 && c0 < 32 * p + 32; c0 += 16) {
+                const int blk = c0 >> 5;
+                float c[16], x[16];
+                const float *src = blk < p ? &G.cf[c0] : &G.ld[c0];
 #pragma unroll
-            for (int i = 0; i < W / 8; ++i) {
-                const uint32_t at = piece(kCT, row, W / 8 * qc + i);
-                const uint4 v = *reinterpret_cast<const uint4 *>(sm + L::V + at);
-                const uint32_t ve[4] = {v.x, v.y, v.z, v.w};
-                uint32_t u[4];
+                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(&c[i]) = *reinterpret_cast<const float4 *>(src + i);
+                ld16(tl + cG + c0, x);
+                tc::wait_ld();
+                uint32_t u[8];
+                if (blk < p) {
+                    const float f = exp_ftz(li + between(G, blk, p));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack2(ve[e]);
-                    const int c = 8 * i + 2 * e;
-                    u[e] = pack2(fmaf(er, y[c], fmaf(skip, f.x, z[c])), fmaf(er, y[c + 1], fmaf(skip, f.y, z[c + 1])));
+                    for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i] * (f * c[2 * i]), x[2 * i + 1] * (f * c[2 * i + 1]));
+                } else {
+                    // (without branches: e^{-inf} above the diagonal, and the value
+                    // there, which may be anything, replaced)
+                    const int d = lane - (c0 & 31);  // the column on the diagonal
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e = exp_ftz(i <= d ? li - c[i] : -INFINITY);
+                        x[i] = fmaf(i <= d ? x[i] : 0.f, e, i == d ? skip : 0.f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
                 }
-                *reinterpret_cast<uint4 *>(sm + L::LO + at) = make_uint4(u[0], u[1], u[2], u[3]);
+                st8(tl + cM + c0 / 2, u);
             }
+            tc::wait_st();
+            give(&r_m);
+            if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
         }
-        handoff();
-        if (aborted) break;
-        if (tid == 0) {
-            if (a.o && (!a.cu || len == kCT)) {
-                for (int x = 0; x < P / 64; ++x) tma_store_5d(&maps.o, sm + L::LO + x * kCT * 128, mt + m * kCT, x, h, mb);
-                tc::bulk_commit();
-            }
-            if (m + 1 < n_chunks) load_v(m + 1);
-        }
-        if (a.o && a.cu && len < kCT) {  // a packed sequence's end: row by row (no chunk follows)
-            bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(sq.row0 + (c_lo + m) * kCT) * a.H + h) * P;
-            for (int i = tid; i < len * (P / 8); i += kNT) {
-                const int r = i / (P / 8), c = i % (P / 8);
-                *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * P + 8 * c) =
-                    *reinterpret_cast<const uint4 *>(sm + L::LO + piece(kCT, r, c));
-            }
-        }
-    }
-    if (last_part && a.S_T && !aborted && row < N) {
-        float *dst = a.S_T + (size_t)bh * N * P + (size_t)row * P + W * qc;
+    } else {
+        // the state that reaches this part: its bf16 copy, and decayed for the first chunk
+        bool ok = true;
+        if (n_chunks > 0) ok = wait(&r_gate[0], 0);
+#pragma unroll 1
+        for (int x = 0; x < HP / 32; ++x) {
+            const int c0 = HP * half + 32 * x;
+            float S[32];
+            start_state<N, P, 32, false>(a.S0, a.part_state, a.part_decay, a.parts, part, bh, row, c0, S);
+            if (n_chunks == 0) {
+                if (last_part && a.S_T && row < N) {
+                    float *dst = a.S_T + (size_t)bh * N * P + (size_t)row * P + c0;
 #pragma unroll
-        for (int i = 0; i < W; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    }
-    if (tid == 0) {  // nothing is left in flight
-        tc::commit(&b_fin);
-        (void)tc::mbar_wait(&b_fin, 0);
-        if (nq) (void)tc::mbar_wait(&ld_q, (nq - 1) & 1);
-        if (nv) (void)tc::mbar_wait(&ld_v, (nv - 1) & 1);
-        for (int s = 0; s < 2; ++s)
-            if (nk[s]) (void)tc::mbar_wait(&ld_k[s], (nk[s] - 1) & 1);
-        tc::bulk_wait();
+                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                }
+            } else {
+                if (row < N) put_row<32>(sm + L::S16, N, row, c0, S);
+                const float gm = gates[0].gamma;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) S[i] *= gm;
+                tc::st_32x32b_x32(tl + cS + c0, S);
+            }
+        }
+        tc::wait_st();
+        if (n_chunks > 0) give(&r_st);
+        const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+        for (int m = 0; ok && m < n_chunks; ++m) {
+            const uint32_t ph = m & 1;
+            const int len = min(kCT, sq.len - (c_lo + m) * kCT);
+            const Gates &G = gates[m % kRing];
+            const bool more = m + 1 < n_chunks;
+            if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&d_yi, ph)) break;
+            tc::fence_after();
+            const float er = G.er[row];
+#pragma unroll 1
+            for (int x = 0; x < HP / 32; ++x) {  // e^{L_i} q_i S
+                float y[32];
+                tc::ld_32x32b_x32(tl + cY + HP * half + 32 * x, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] *= er;
+                tc::st_32x32b_x32(tl + cY + HP * half + 32 * x, y);
+            }
+            tc::wait_st();
+            give(&r_ys);
+            // the state behind this chunk
+            if ((more && !wait(&r_gate[(m + 1) % kRing], par(m + 1, kRing))) || !wait(&d_s, ph)) break;
+            tc::fence_after();
+            if (more) {
+                const float gm = gates[(m + 1) % kRing].gamma;
+#pragma unroll 1
+                for (int x = 0; x < HP / 32; ++x) {
+                    float S[32];
+                    const int c0 = HP * half + 32 * x;
+                    tc::ld_32x32b_x32(tl + cS + c0, S);
+                    tc::wait_ld();
+                    if (row < N) put_row<32>(sm + L::S16, N, row, c0, S);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) S[i] *= gm;
+                    tc::st_32x32b_x32(tl + cS + c0, S);
+                }
+                tc::wait_st();
+                give(&r_st);
+            } else if (last_part && a.S_T) {
+#pragma unroll 1
+                for (int x = 0; x < HP / 32; ++x) {
+                    float S[32];
+                    const int c0 = HP * half + 32 * x;
+                    tc::ld_32x32b_x32(tl + cS + c0, S);
+                    tc::wait_ld();
+                    float *dst = a.S_T + (size_t)bh * N * P + (size_t)row * P + c0;
+                    if (row < N)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                }
+            }
+            if (!wait(&d_y, ph)) break;
+            tc::fence_after();
+            bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(sq.row0 + (c_lo + m) * kCT + row) * a.H + h) * P + HP * half;
+#pragma unroll 1
+            for (int x = 0; x < HP / 32; ++x) {
+                float y[32];
+                tc::ld_32x32b_x32(tl + cY + HP * half + 32 * x, y);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = pack2(y[16 * e + 2 * i], y[16 * e + 2 * i + 1]);
+                    if (row < len) store32(o + 32 * x + 16 * e, u, wide);
+                }
+            }
+            give(&r_o);
+            if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
+        }
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (tid == 0 && dead) record_status(a.status, GDN2_ERR_TIMEOUT);
+    if (warp == 16) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
@@ -387,6 +462,7 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t ld[2], b_s[2], b_fin;
     __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, qc = warp >> 2, row = 32 * p + lane;
     const int np = LOCAL ? a.parts - 1 : a.parts;
@@ -408,28 +484,30 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         uint64_t *bars[] = {&ld[0], &ld[1], &b_s[0], &b_s[1], &b_fin};
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
         tc::fence_mbar_init();
+        dead = 0;
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
 
-    int nl[2] = {0, 0};
+    int nl = 0;
     auto load = [&](int m) {
+        ++nl;
+        if (!elect()) return;
         const int s = m & 1, t = mt + chunk_of(m) * kCT;
         tc::mbar_expect_tx(&ld[s], L::AB + L::XB);
+#pragma unroll
         for (int x = 0; x < N / 64; ++x)
-            tc::tma_load_5d(sm + (s ? L::A1 : L::A0) + x * kCT * 128, &maps.a, 0, t, x, g, mb, &ld[s]);
+            tc::tma_load_5d(sm + L::A0 + s * L::AB + x * kCT * 128, &maps.a, 0, t, x, g, mb, &ld[s]);
+#pragma unroll
         for (int x = 0; x < P / 64; ++x)
-            tc::tma_load_5d(sm + (s ? L::X1 : L::X0) + x * kCT * 128, &maps.x, 0, t, x, h, mb, &ld[s]);
-        ++nl[s];
+            tc::tma_load_5d(sm + L::X0 + s * L::XB + x * kCT * 128, &maps.x, 0, t, x, h, mb, &ld[s]);
     };
     bool bad = false, aborted = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!tc::mbar_wait(bar, parity)) {
-            bad = true;
-            record_status(a.status, GDN2_ERR_TIMEOUT);
-        }
+        if (!wait_bar(bar, parity, &dead)) bad = true;
+        __syncwarp();
     };
     auto handoff = [&]() {
         tc::fence_async_smem();
@@ -437,7 +515,7 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         aborted = __syncthreads_or(bad);
         tc::fence_after();
     };
-    if (tid == 0) {
+    if (warp == 0) {
         if (n_chunks > 0) load(0);
         if (n_chunks > 1) load(1);
     }
@@ -457,7 +535,7 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         Gates &G = gates[m & 1];
         form_gates(G, g_la, g_dt, gt, 1, LOCAL && !REV ? carry : 0.f);
         if (LOCAL) {
-            if (REV) G.er[gt] *= __expf(carry);
+            if (REV) G.er[gt] *= exp_ftz(carry);
             asm volatile("bar.sync 1, 128;\n" ::: "memory");
             carry = fmaxf(carry + G.total, 2.f * kLogMin);  // (as good as -inf; kept finite)
         }
@@ -488,18 +566,18 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         const uint32_t ph2 = (m >> 1) & 1;
         unsigned char *A = sm + (s ? L::A1 : L::A0), *X = sm + (s ? L::X1 : L::X0),
                       *LOW = sm + (LOCAL && s ? L::LO1 : L::LO0);
-        if (!LOCAL && tid == 0) {
+        if (!LOCAL && warp == 0 && elect()) {
             tc::bulk_store(a.images + ((size_t)(sq.slot + chunk_of(m)) * a.H + h) * IMG, sm + L::S16, IMG);
             tc::bulk_commit();
         }
         wait(&ld[s], ph2);
         if (a.cu && len < kCT) zero_tail(X, P / 64, len, tid, kNT);
-        scale_hi_lo<N>(A, LOW, REV ? gates[s].er : gates[s].wt, len, tid);
+        scale_hi_lo<N, kNT>(A, LOW, REV ? gates[s].er : gates[s].wt, len, tid);
         if (gt >= 0 && m + 1 < n_chunks) gates_of(m + 1);
-        if (!LOCAL && tid == 0) tc::bulk_wait_read();
+        if (!LOCAL && warp == 0 && elect()) tc::bulk_wait_read();
         handoff();
         if (aborted) break;
-        if (tid == 0) {
+        if (warp == 0 && elect()) {
             mma_tiles<false, false>(tm, A, kCT, X, kCT, kCT / 16, idS, !LOCAL || m > 0);
             mma_tiles<false, false>(tm, LOW, kCT, X, kCT, kCT / 16, idS, true);
             tc::commit(&b_s[s]);
@@ -507,13 +585,13 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         if (LOCAL) {  // the product runs under the next chunk's scaling; its tiles are free when it is done
             if (m > 0) {
                 wait(&b_s[s ^ 1], ((m - 1) >> 1) & 1);
-                if (tid == 0 && m + 1 < n_chunks) load(m + 1);
+                if (warp == 0 && m + 1 < n_chunks) load(m + 1);
             }
             continue;
         }
         wait(&b_s[s], ph2);
         tc::fence_after();
-        if (tid == 0 && m + 2 < n_chunks) load(m + 2);
+        if (warp == 0 && m + 2 < n_chunks) load(m + 2);
         ldw<W>(tl + W * qc, S);
         tc::wait_ld();
         if (m + 1 < n_chunks) {
@@ -545,16 +623,19 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
 #pragma unroll
         for (int i = 0; i < W; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     }
-    if (LOCAL && gt == 0) a.part_decay[(size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)] = __expf(carry);
-    if (tid == 0) {
-        tc::commit(&b_fin);
+    if (LOCAL && gt == 0) a.part_decay[(size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)] = exp_ftz(carry);
+    if (warp == 0) {  // nothing is left in flight
+        if (elect()) {
+            tc::commit(&b_fin);
+            tc::bulk_wait();
+        }
         (void)tc::mbar_wait(&b_fin, 0);
-        for (int s = 0; s < 2; ++s)
-            if (nl[s]) (void)tc::mbar_wait(&ld[s], (nl[s] - 1) & 1);
-        tc::bulk_wait();
+        if (nl > 0) (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
+        if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
     }
     tc::fence_before();
     __syncthreads();
+    if (tid == 0 && dead) record_status(a.status, GDN2_ERR_TIMEOUT);
     if (warp == 0) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 128);
@@ -587,8 +668,7 @@ cudaError_t fwd_np(const ScanArgs &a, cudaStream_t s) {
     ChainMaps cm;
     const int MB = a.cu ? 1 : a.B;
     if (!scan_tile_map(&m.q, a.q, a.ldq, MB, a.T, a.G, N) || !scan_tile_map(&m.k, a.k, a.ldk, MB, a.T, a.G, N) ||
-        !scan_tile_map(&m.v, a.v, a.ldv, MB, a.T, a.H, P) ||
-        (a.o && !scan_tile_map(&m.o, a.o, (long long)a.H * P, MB, a.T, a.H, P)))
+        !scan_tile_map(&m.v, a.v, a.ldv, MB, a.T, a.H, P))
         return cudaErrorInvalidValue;
     cudaError_t e;
     cm.a = m.k;
@@ -604,7 +684,7 @@ cudaError_t fwd_np(const ScanArgs &a, cudaStream_t s) {
     auto kernel = fwd_kernel<N, P>;
     constexpr int bytes = FwdSmem<N, P>::BYTES;
     if ((e = big_smem(kernel, bytes)) != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.B * a.H * a.parts), kNT, bytes, s>>>(a, m);
+    kernel<<<(unsigned)(a.B * a.H * a.parts), kFwdThreads, bytes, s>>>(a, m);
     return cudaGetLastError();
 }
 

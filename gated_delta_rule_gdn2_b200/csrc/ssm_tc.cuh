@@ -43,6 +43,48 @@ __device__ __forceinline__ void tma_store_5d(const void *map, const void *src, i
                  : "memory");
 }
 
+// e^x by the fast base-2 exponential, results below 2^-126 taken as 0 (2
+// instructions; x = -inf gives 0).
+__device__ __forceinline__ float exp_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+// A bounded wait for the phase `parity` of a barrier: false when it ran out
+// here, or (dead != 0) in any thread of the block.  Kept to a dozen
+// instructions: the kernels hold dozens of waits, and their code has to stay
+// within the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *dead) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .u32 n, d;\nmov.u32 n, 0;\n"
+        "AGAIN:\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "@p bra DONE;\n"
+        "ld.volatile.shared.u32 d, [%3];\n"
+        "add.u32 n, n, 1;\n"
+        "setp.ge.u32 p, n, %4;\n"
+        "@p mov.u32 d, 1;\n"
+        "setp.eq.u32 p, d, 0;\n"
+        "@p bra AGAIN;\n"
+        "st.volatile.shared.u32 [%3], d;\n"
+        "setp.ne.u32 p, d, d;\n"
+        "DONE:\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_addr(bar)), "r"(parity), "r"(tc::smem_addr(dead)), "n"(tc::kWaitLimit)
+        : "memory");
+    return ok != 0;
+}
+// One lane of a converged warp (products and copies are issued by the warp
+// that runs their loop as a whole: its operands stay uniform).
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.b32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // D (+)= A B with A [128][K] bf16 in tensor memory (two values a column).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -115,9 +157,9 @@ __device__ __forceinline__ void put_row(unsigned char *tile, int R, int r, int c
 //   cf   e^{log decay from behind the token to the block's end} (FWD: times dt)
 //   er   e^{log decay from the chunk's start through the token}
 //   wt   e^{log decay from behind the token to the chunk's end} (FWD: times dt)
-//   dt   the step size
+//   ld   l less the log of the step size (so e^{l_i - ld_j} holds dt_j)
 struct alignas(16) Gates {  // (read in 16-byte pieces, two side by side)
-    float l[kCT], cf[kCT], er[kCT], wt[kCT], dt[kCT];
+    float l[kCT], cf[kCT], er[kCT], wt[kCT], ld[kCT];
     float bs[4];    // the blocks' log decays
     float gamma;    // the chunk's decay
     float total;    // its log
@@ -135,19 +177,75 @@ __device__ __forceinline__ void form_gates(Gates &g, float la, float dt, int t, 
     }
     const float behind = __shfl_down_sync(0xffffffffu, dn, 1), s = lane < 31 ? behind : 0.f;
     g.l[t] = up;
-    g.cf[t] = __expf(s) * dt;
-    g.dt[t] = dt;
+    g.cf[t] = exp_ftz(s) * dt;
     if (lane == 31) g.bs[w] = up;
     asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
     const float b0 = g.bs[0], b1 = g.bs[1], b2 = g.bs[2], b3 = g.bs[3];
     const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
     const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
-    g.er[t] = __expf(pre + up);
-    g.wt[t] = __expf(s + post + carry) * dt;
+    g.er[t] = exp_ftz(pre + up);
+    g.wt[t] = exp_ftz(s + post + carry) * dt;
     if (t == 0) {
         const float all = b0 + b1 + b2 + b3;
-        g.gamma = __expf(all);
+        g.gamma = exp_ftz(all);
         g.total = all;
+    }
+}
+// The same by one warp, four tokens a lane, from token t0 of a sequence of len
+// tokens whose values lie `stride` elements apart from `first` on.
+__device__ __forceinline__ void form_gates_warp(Gates &g, const void *la, const void *dt, size_t first, int stride, int t0,
+                                                int len, int lane) {
+    float x[4], d[4], up[4], dn[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int t = t0 + 4 * lane + e;
+        const size_t r = first + (size_t)t * stride;
+        x[e] = t < len ? fmaxf(__bfloat162float(static_cast<const bf16 *>(la)[r]), kLogMin) : 0.f;
+        d[e] = t < len ? __bfloat162float(static_cast<const bf16 *>(dt)[r]) : 0.f;
+    }
+    up[0] = x[0];
+    dn[3] = x[3];
+#pragma unroll
+    for (int e = 1; e < 4; ++e) {
+        up[e] = up[e - 1] + x[e];
+        dn[3 - e] = dn[4 - e] + x[3 - e];
+    }
+    // within the blocks of 32 tokens (8 lanes), then across them
+    float a = up[3], c = dn[0];
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, a, m, 8), z = __shfl_down_sync(0xffffffffu, c, m, 8);
+        if ((lane & 7) >= m) a += y;
+        if ((lane & 7) + m < 8) c += z;
+    }
+    float before = __shfl_up_sync(0xffffffffu, a, 1, 8), behind = __shfl_down_sync(0xffffffffu, c, 1, 8);
+    if ((lane & 7) == 0) before = 0.f;
+    if ((lane & 7) == 7) behind = 0.f;
+    const float b0 = __shfl_sync(0xffffffffu, a, 7), b1 = __shfl_sync(0xffffffffu, a, 15), b2 = __shfl_sync(0xffffffffu, a, 23),
+                b3 = __shfl_sync(0xffffffffu, a, 31);
+    const int w = lane >> 3;
+    const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
+    const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
+    float l[4], cf[4], er[4], wt[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float s = behind + (e < 3 ? dn[e + 1] : 0.f);
+        l[e] = before + up[e];
+        cf[e] = exp_ftz(s) * d[e];
+        er[e] = exp_ftz(pre + l[e]);
+        wt[e] = exp_ftz(s + post) * d[e];
+    }
+    *reinterpret_cast<float4 *>(&g.l[4 * lane]) = make_float4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<float4 *>(&g.cf[4 * lane]) = make_float4(cf[0], cf[1], cf[2], cf[3]);
+    *reinterpret_cast<float4 *>(&g.er[4 * lane]) = make_float4(er[0], er[1], er[2], er[3]);
+    *reinterpret_cast<float4 *>(&g.wt[4 * lane]) = make_float4(wt[0], wt[1], wt[2], wt[3]);
+    // (a step of zero: ld = inf, a factor of 0; a negative one does not occur)
+    *reinterpret_cast<float4 *>(&g.ld[4 * lane]) =
+        make_float4(l[0] - __logf(d[0]), l[1] - __logf(d[1]), l[2] - __logf(d[2]), l[3] - __logf(d[3]));
+    if ((lane & 7) == 7) g.bs[w] = a;
+    if (lane == 0) {
+        g.total = b0 + b1 + b2 + b3;
+        g.gamma = exp_ftz(b0 + b1 + b2 + b3);
     }
 }
 // log decay of the blocks strictly between block a and block b > a
@@ -171,28 +269,42 @@ __device__ __forceinline__ void zero_tail(unsigned char *tile, int nblk, int len
 // Rows of a [128][64 w] tile scaled by f[row], in two bf16 parts whose sum
 // carries 16 bits: the parts of the first go in place, of the rest to `lo`.
 // Rows from len on become zero whatever they hold.
-template <int D>
+template <int D, int NT>
 __device__ __forceinline__ void scale_hi_lo(unsigned char *hi, unsigned char *lo, const float *f, int len, int tid) {
-    constexpr int PPR = D / 8;  // pieces a row
+    // eight consecutive lanes take the eight pieces of one 128-byte row; a
+    // thread's pieces lie NT / 8 rows apart, four loaded ahead of their use
+    constexpr int PER = kCT * (D / 8) / NT;
+    static_assert(PER % 4 == 0 || PER == 2, "pieces of a thread");
+    constexpr int U = PER % 4 == 0 ? 4 : 2;
+    const bool whole = len == kCT;
+#pragma unroll 1
+    for (int i0 = 0; i0 < PER; i0 += U) {
+        uint4 x[U];
+        float w[U];
 #pragma unroll
-    for (int i = 0; i < kCT * PPR / kNT; ++i) {
-        // eight consecutive lanes take the eight pieces of one 128-byte row
-        const int id = tid + i * kNT, blk = id / (kCT * 8), r = (id / 8) % kCT;
-        const uint32_t at = (uint32_t)(blk * (kCT * 128) + r * 128 + (id % 8) * 16);
-        uint4 x = *reinterpret_cast<const uint4 *>(hi + at), y;
-        const float w = f[r];
-        uint32_t *xe = reinterpret_cast<uint32_t *>(&x), *ye = reinterpret_cast<uint32_t *>(&y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 v = unpack2(xe[e]);
-            const float a = v.x * w, b = v.y * w;
-            const uint32_t h = pack2(a, b);
-            const float2 hf = unpack2(h);
-            xe[e] = r < len ? h : 0u;
-            ye[e] = r < len ? pack2(a - hf.x, b - hf.y) : 0u;
+        for (int i = 0; i < U; ++i) {
+            const int id = tid + (i0 + i) * NT;
+            x[i] = *reinterpret_cast<const uint4 *>(hi + id * 16);
+            w[i] = f[(id / 8) % kCT];
         }
-        *reinterpret_cast<uint4 *>(hi + at) = x;
-        *reinterpret_cast<uint4 *>(lo + at) = y;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int id = tid + (i0 + i) * NT;
+            uint4 y;
+            uint32_t *xe = reinterpret_cast<uint32_t *>(&x[i]), *ye = reinterpret_cast<uint32_t *>(&y);
+            const float2 w2 = make_float2(w[i], w[i]);
+            const bool keep = whole || (id / 8) % kCT < len;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = unpack2(xe[e]), t = __fmul2_rn(v, w2);
+                const uint32_t h = pack2(t.x, t.y);
+                const float2 hf = unpack2(h), r = __ffma2_rn(hf, make_float2(-1.f, -1.f), t);
+                xe[e] = keep ? h : 0u;
+                ye[e] = keep ? pack2(r.x, r.y) : 0u;
+            }
+            *reinterpret_cast<uint4 *>(hi + id * 16) = x[i];
+            *reinterpret_cast<uint4 *>(lo + id * 16) = y;
+        }
     }
 }
 
