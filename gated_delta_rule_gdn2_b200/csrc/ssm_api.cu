@@ -3,6 +3,7 @@
 #include "gdn2.h"
 
 #include <algorithm>
+#include <cmath>
 
 #include "ssm.h"
 
@@ -83,8 +84,13 @@ Plan plan(const void *cu, int B, int T, int H, int G, int dk, int dv, int dtype,
     p.splits = 1;
     if (bwd) {
         const int hpg = H / G;
-        while (p.splits < hpg && slots * G * p.splits < 2LL * device_sm_count()) p.splits *= 2;
-        p.splits = std::min(p.splits, hpg);
+        // heads of a group in one block after another, unless the blocks then
+        // leave a fifth of the GPU idle (several runs' sums cost a pass over
+        // dq and dk in fp32)
+        const double sms = device_sm_count();
+        auto cost = [&](int n) { return std::ceil(slots * G * n / sms) * ((hpg + n - 1) / n); };
+        for (int n = 2; n <= hpg; n *= 2)
+            if (cost(n) < 0.8 * cost(p.splits)) p.splits = n;
         p.grads = at; at += r256((size_t)slots * H * img);
         p.states = at; at += own_states ? r256((size_t)slots * H * img) : 0;
         p.dqk = at; at += p.splits > 1 ? r256((size_t)2 * p.splits * rows * G * dk * 4) : 0;

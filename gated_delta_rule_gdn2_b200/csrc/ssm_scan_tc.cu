@@ -34,7 +34,7 @@ namespace {
 using tct::mma_tiles;
 
 struct Maps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // The state (or gradient) that reaches part `part`, W columns of row r.
@@ -70,9 +70,9 @@ __device__ __forceinline__ float token(const void *p, size_t i) { return __bfloa
 // forms the decay factors up to four chunks ahead, and the other sixteen work
 // in two groups that meet only through mbarriers, so that the state-free half
 // of chunk m + 1 runs beside the state's half of chunk m:
-//   A (warps 0..7)   the two parts of the scaled k in shared memory; M from G
-//   B (warps 8..15)  q S scaled by e^L in place (M v is added to it); the
-//                    state's bf16 copy and its decay; o
+//   A (warps 0..7)   the two parts of the scaled k in shared memory (64 tokens
+//                    at a time: the second part's tile is half a chunk's); M
+//   B (warps 8..15)  o from q S and M v; the state's bf16 copy and its decay
 // A thread of either group owns a row (token or key channel) of tensor memory
 // and half of its columns.
 
@@ -83,34 +83,24 @@ struct FwdSmem {
     static constexpr int QB = kCT * N * 2, VB = kCT * P * 2;
     // (At N = 64 the state's product reads 128 rows of its left operand; the
     // upper 64 are whatever block follows, and go to rows of S that nothing reads.)
-    static constexpr int LO = 0, K0 = QB, K1 = K0 + QB, Q = K1 + QB, V = Q + QB, S16 = V + VB, G = S16 + N * P * 2,
-                         END = G + kRing * (int)sizeof(Gates);
+    // The o tile is written over this chunk's q (at N = 64 it may be larger, and has its own place).
+    static constexpr bool OVER_Q = QB >= VB;
+    static constexpr int LO = 0, K = QB / 2, Q = K + 2 * QB, V = Q + 2 * QB, S16 = V + VB, O = S16 + N * P * 2,
+                         G = O + (OVER_Q ? 0 : VB), END = G + kRing * (int)sizeof(Gates);
     static constexpr int BYTES = END + 1024;
 };
-
-// 32 bytes of a row (16 values as bf16) to global memory.
-__device__ __forceinline__ void store32(bf16 *dst, const uint32_t (&u)[8], bool wide) {
-    if (wide) {  // whole sectors
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-    }
-}
 
 template <int N, int P>
 __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const __grid_constant__ Maps maps) {
     using L = FwdSmem<N, P>;
     constexpr int HP = P / 2;  // columns of a thread in a P-column row
-    constexpr uint32_t cS = 0, cG = 128, cY = 256, cM = 384;  // tensor-memory columns
+    constexpr uint32_t cS = 0, cG = 128, cY = 256, cY2 = 384;  // tensor-memory columns (M lies over G)
     constexpr uint32_t idG = tc::idesc_bf16(128, 128, false, false), idY = tc::idesc_bf16(128, P, false, true),
                        idS = tc::idesc_bf16(128, P, true, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     // tiles landed; products done; hand-overs of the groups (one arrival a warp)
-    __shared__ uint64_t ld_q, ld_k[2], ld_v, d_g, d_yi, d_s, d_y, r_hl, r_m, r_ys, r_st, r_o, r_gate[kRing], r_gfree[kRing], d_fin;
+    __shared__ uint64_t ld_qk[2], ld_v, d_g, d_yi, d_s1, d_s, d_y, r_hl, r_hl2, r_m, r_st, r_o, r_tail, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
@@ -128,9 +118,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
 
     if (warp == 16) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        uint64_t *one[] = {&ld_q, &ld_k[0], &ld_k[1], &ld_v, &d_g, &d_yi, &d_s, &d_y, &d_fin};
+        uint64_t *one[] = {&ld_qk[0], &ld_qk[1], &ld_v, &d_g, &d_yi, &d_s1, &d_s, &d_y, &d_fin};
         for (uint64_t *x : one) tc::mbar_init(x, 1);
-        uint64_t *eight[] = {&r_hl, &r_m, &r_ys, &r_st, &r_o};
+        uint64_t *eight[] = {&r_hl, &r_hl2, &r_m, &r_st, &r_o, &r_tail};
         for (uint64_t *x : eight) tc::mbar_init(x, 8);
         for (int i = 0; i < kRing; ++i) {
             tc::mbar_init(&r_gate[i], 1);
@@ -153,27 +143,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     };
+    auto tile_o = [&](int m) { return sm + (L::OVER_Q ? L::Q + (m & 1) * L::QB : L::O); };
     // chunk m's parity on a barrier that completes once a chunk, or once in R chunks
     auto par = [](int m, int R) { return (uint32_t)(m / R) & 1u; };
 
     if (warp == 16) {
         if (n_chunks > 0) {
-            int nq = 0, nk = 0, nv = 0;  // loads issued
-            auto load_q = [&](int m) {
-                ++nq;
+            int nqk = 0, nv = 0;  // loads issued
+            auto load_qk = [&](int m) {
+                ++nqk;
                 if (!elect()) return;
-                tc::mbar_expect_tx(&ld_q, L::QB);
+                uint64_t *bar = &ld_qk[m & 1];
+                unsigned char *q = sm + L::Q + (m & 1) * L::QB, *k = sm + L::K + (m & 1) * L::QB;
+                tc::mbar_expect_tx(bar, 2 * L::QB);
 #pragma unroll
-                for (int x = 0; x < N / 64; ++x) tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt + m * kCT, x, g, mb, &ld_q);
-            };
-            auto load_k = [&](int m) {
-                ++nk;
-                if (!elect()) return;
-                uint64_t *bar = &ld_k[m & 1];
-                unsigned char *dst = sm + L::K0 + (m & 1) * L::QB;
-                tc::mbar_expect_tx(bar, L::QB);
-#pragma unroll
-                for (int x = 0; x < N / 64; ++x) tc::tma_load_5d(dst + x * kCT * 128, &maps.k, 0, mt + m * kCT, x, g, mb, bar);
+                for (int x = 0; x < N / 64; ++x) {
+                    tc::tma_load_5d(q + x * kCT * 128, &maps.q, 0, mt + m * kCT, x, g, mb, bar);
+                    tc::tma_load_5d(k + x * kCT * 128, &maps.k, 0, mt + m * kCT, x, g, mb, bar);
+                }
             };
             auto load_v = [&](int m) {
                 ++nv;
@@ -184,24 +171,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
             };
             auto product_G = [&](int m) {
                 if (!elect()) return;
-                mma_tiles<true, true>(tm + cG, sm + L::Q, kCT, sm + L::K0 + (m & 1) * L::QB, kCT, N / 16, idG, false);
+                mma_tiles<true, true>(tm + cG, sm + L::Q + (m & 1) * L::QB, kCT, sm + L::K + (m & 1) * L::QB, kCT, N / 16, idG, false);
                 tc::commit(&d_g);
             };
-            load_q(0);
-            load_k(0);
+            // half x of the state's product: 64 tokens
+            auto product_S = [&](int m, int x, uint64_t *done) {
+                if (!elect()) return;
+                const unsigned char *k = sm + L::K + (m & 1) * L::QB + x * 64 * 128, *v = sm + L::V + x * 64 * 128;
+                mma_tiles<false, false>(tm + cS, k, kCT, v, kCT, 4, idS, true);
+                mma_tiles<false, false>(tm + cS, sm + L::LO, 64, v, kCT, 4, idS, true);
+                if (x) tc::bulk_wait_read();  // (S16's image has been read: the commit lets group B overwrite it)
+                tc::commit(done);
+            };
+            load_qk(0);
             load_v(0);
-            if (n_chunks > 1) load_k(1);
-            bool ok = wait(&ld_q, 0) && wait(&ld_k[0], 0);
+            if (n_chunks > 1) load_qk(1);
+            bool ok = wait(&ld_qk[0], 0);
             if (ok) product_G(0);
-            int m = 0;
-            for (; ok && m < n_chunks; ++m) {
+            for (int m = 0; ok && m < n_chunks; ++m) {
                 const uint32_t ph = m & 1;
                 const bool more = m + 1 < n_chunks;
-                if (!(ok = wait(&r_st, ph) && (m == 0 || wait(&r_o, ph ^ 1)))) break;
+                if (!(ok = wait(&r_st, ph) && wait(&r_hl, ph) && wait(&ld_v, ph))) break;
                 tc::fence_after();
-                if (m > 0) load_v(m);
+                product_S(m, 0, &d_s1);
                 if (elect()) {
-                    mma_tiles<true, false>(tm + cY, sm + L::Q, kCT, sm + L::S16, N, N / 16, idY, false);
+                    mma_tiles<true, false>(tm + cY, sm + L::Q + (m & 1) * L::QB, kCT, sm + L::S16, N, N / 16, idY, false);
                     tc::commit(&d_yi);
                     if (a.states) {  // the state at the chunk's start, as it lies here
                         tc::bulk_store(static_cast<unsigned char *>(a.states) +
@@ -210,32 +204,36 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                         tc::bulk_commit();
                     }
                 }
-                if (!(ok = wait(&r_hl, ph) && wait(&ld_v, ph))) break;
-                tc::fence_after();
-                if (elect()) {
-                    mma_tiles<false, false>(tm + cS, sm + L::K0 + (m & 1) * L::QB, kCT, sm + L::V, kCT, kCT / 16, idS, true);
-                    mma_tiles<false, false>(tm + cS, sm + L::LO, kCT, sm + L::V, kCT, kCT / 16, idS, true);
-                    tc::bulk_wait_read();  // (the commit lets group B overwrite S16)
-                    tc::commit(&d_s);
+                if (m > 0 && more) {  // the chunk before: its q, k and o are out of the way
+                    if (elect()) tc::bulk_wait_read();
+                    __syncwarp();
+                    load_qk(m + 1);
                 }
-                if (more) {
-                    if (!(ok = wait(&d_yi, ph))) break;
-                    load_q(m + 1);
-                }
-                if (!(ok = wait(&r_m, ph) && wait(&r_ys, ph))) break;
+                if (!(ok = wait(&r_m, ph))) break;
                 tc::fence_after();
                 if (elect()) {
                     const uint64_t v0 = tct::mnmaj(sm + L::V, kCT, 0);
 #pragma unroll
                     for (int x = 0; x < kCT / 16; ++x)
-                        mma_ts(tm + cY, tm + cM + 8 * x, v0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, true);
+                        mma_ts(tm + cY2, tm + cG + 8 * x + (x < 4 ? 0 : 32), v0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, x > 0);
                     tc::commit(&d_y);
                 }
+                if (!(ok = wait(&r_hl2, ph))) break;
+                tc::fence_after();
+                product_S(m, 1, &d_s);
                 if (more) {
-                    if (!(ok = wait(&ld_q, ph ^ 1) && wait(&ld_k[(m + 1) & 1], par(m + 1, 2)))) break;
-                    product_G(m + 1);
+                    if (!(ok = wait(&ld_qk[ph ^ 1], par(m + 1, 2)))) break;
+                    product_G(m + 1);  // (behind M v, which reads M where G goes)
                     if (!(ok = wait(&d_s, ph))) break;
-                    if (m + 2 < n_chunks) load_k(m + 2);
+                    load_v(m + 1);
+                }
+                if (!(ok = wait(&r_o, ph))) break;
+                if (elect()) {  // (a packed sequence's end is stored row by row)
+                    if (!a.cu || sq.len - (c_lo + m) * kCT >= kCT)
+#pragma unroll
+                        for (int x = 0; x < P / 64; ++x)
+                            tma_store_5d(&maps.o, tile_o(m) + x * kCT * 128, mt + m * kCT, x, h, mb);
+                    tc::bulk_commit();
                 }
             }
             if (elect()) {  // nothing is left in flight
@@ -243,10 +241,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 tc::bulk_wait();
             }
             (void)tc::mbar_wait(&d_fin, 0);
-            (void)tc::mbar_wait(&ld_q, (nq - 1) & 1);
             (void)tc::mbar_wait(&ld_v, (nv - 1) & 1);
-            (void)tc::mbar_wait(&ld_k[0], ((nk - 1) >> 1) & 1);
-            if (nk > 1) (void)tc::mbar_wait(&ld_k[1], ((nk - 2) >> 1) & 1);
+            (void)tc::mbar_wait(&ld_qk[0], ((nqk - 1) >> 1) & 1);
+            if (nqk > 1) (void)tc::mbar_wait(&ld_qk[1], ((nqk - 2) >> 1) & 1);
         }
         __syncwarp();
     } else if (warp == 17) {
@@ -259,34 +256,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     } else if (warp < 8) {
         const int gt = tid;  // 0 .. 255
         const float skip = a.skip ? a.skip[h] : 0.f;
-        {  // (blocks j > i of M stay zero)
-            const uint32_t z[16] = {0};
-            for (int blk = 2 * half; blk < 2 * half + 2; ++blk)
-                if (blk > p) st16(tl + cM + 16 * blk, z);
-            tc::wait_st();
-        }
         for (int m = 0; m < n_chunks; ++m) {
             const uint32_t ph = m & 1;
             const int len = min(kCT, sq.len - (c_lo + m) * kCT);
             const Gates &G = gates[m % kRing];
-            // (the second part's tile was last read by the product before)
+            // (the second part's tile was last read by the state's product before)
             if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&d_g, ph) || (m > 0 && !wait(&d_s, ph ^ 1))) break;
-            scale_hi_lo<N, 256>(sm + (m & 1 ? L::K1 : L::K0), sm + L::LO, G.wt, len, gt);
+            unsigned char *K = sm + L::K + (m & 1) * L::QB;
+            scale_hi_lo<N, 256, 64>(K, sm + L::LO, G.wt, 0, len, gt);
             if (a.cu && len < kCT) {
                 if (!wait(&ld_v, ph)) break;
                 zero_tail(sm + L::V, P / 64, len, gt, 256);
             }
             give(&r_hl);
             // M = G masked and decayed, skip on its diagonal: row i = row,
-            // columns 64 half ..  (Column factors are fetched whole before the
+            // columns 64 half .., written over the columns of G that this thread
+            // has read (64 half + 0 .. 31).  (Column factors are fetched whole before the
             // tile's values: a shared load takes hundreds of cycles while the
             // products stream their operands.)
             tc::fence_after();
-            if (m > 0 && !wait(&d_y, ph ^ 1)) break;  // the M before has been read
-            tc::fence_after();
             const float li = G.l[row];
 #pragma unroll 1
-            for (int c0 = 64 * half; c0 < 64 * half + 64 && c0 < 32 * p + 32; c0 += 16) {
+            for (int c0 = 64 * half; c0 < 64 * half + 64; c0 += 16) {
                 const int blk = c0 >> 5;
                 float c[16], x[16];
                 const float *src = blk < p ? &G.cf[c0] : &G.ld[c0];
@@ -295,7 +286,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 ld16(tl + cG + c0, x);
                 tc::wait_ld();
                 uint32_t u[8];
-                if (blk < p) {
+                if (blk > p) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = 0u;
+                } else if (blk < p) {
                     const float f = exp_ftz(li + between(G, blk, p));
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i] * (f * c[2 * i]), x[2 * i + 1] * (f * c[2 * i + 1]));
@@ -311,10 +305,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
                 }
-                st8(tl + cM + c0 / 2, u);
+                st8(tl + cG + 64 * half + (c0 & 63) / 2, u);
             }
             tc::wait_st();
             give(&r_m);
+            if (!wait(&d_s1, ph)) break;  // the first half's second part has been read
+            scale_hi_lo<N, 256, 64>(K, sm + L::LO, G.wt, 64, len, gt);
+            give(&r_hl2);
             if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
         }
     } else {
@@ -342,26 +339,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
         }
         tc::wait_st();
         if (n_chunks > 0) give(&r_st);
-        const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
         for (int m = 0; ok && m < n_chunks; ++m) {
             const uint32_t ph = m & 1;
             const int len = min(kCT, sq.len - (c_lo + m) * kCT);
             const Gates &G = gates[m % kRing];
             const bool more = m + 1 < n_chunks;
-            if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&d_yi, ph)) break;
+            if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&d_yi, ph) || !wait(&d_y, ph)) break;
             tc::fence_after();
+            unsigned char *O = tile_o(m);
             const float er = G.er[row];
 #pragma unroll 1
-            for (int x = 0; x < HP / 32; ++x) {  // e^{L_i} q_i S
-                float y[32];
-                tc::ld_32x32b_x32(tl + cY + HP * half + 32 * x, y);
+            for (int x = 0; x < HP / 16; ++x) {  // o
+                const int c0 = HP * half + 16 * x;
+                float y[16], z[16];
+                ld16(tl + cY + c0, y);
+                ld16(tl + cY2 + c0, z);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] *= er;
-                tc::st_32x32b_x32(tl + cY + HP * half + 32 * x, y);
+                for (int i = 0; i < 16; ++i) y[i] = fmaf(er, y[i], z[i]);
+                put_row<16>(O, kCT, row, c0, y);
             }
-            tc::wait_st();
-            give(&r_ys);
+            if (a.cu && len < kCT) {  // a packed sequence's end: row by row
+                give(&r_tail);
+                if (!wait(&r_tail, 0)) break;
+                bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(sq.row0 + (c_lo + m) * kCT) * a.H + h) * P;
+                for (int i = tid - 256; i < len * (P / 8); i += 256) {
+                    const int r = i / (P / 8), c = i % (P / 8);
+                    *reinterpret_cast<uint4 *>(o + (size_t)r * a.H * P + 8 * c) = *reinterpret_cast<const uint4 *>(O + piece(kCT, r, c));
+                }
+            }
+            give(&r_o);
+            if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
             // the state behind this chunk
             if ((more && !wait(&r_gate[(m + 1) % kRing], par(m + 1, kRing))) || !wait(&d_s, ph)) break;
             tc::fence_after();
@@ -394,24 +402,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                             *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
                 }
             }
-            if (!wait(&d_y, ph)) break;
-            tc::fence_after();
-            bf16 *o = static_cast<bf16 *>(a.o) + ((size_t)(sq.row0 + (c_lo + m) * kCT + row) * a.H + h) * P + HP * half;
-#pragma unroll 1
-            for (int x = 0; x < HP / 32; ++x) {
-                float y[32];
-                tc::ld_32x32b_x32(tl + cY + HP * half + 32 * x, y);
-                tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = pack2(y[16 * e + 2 * i], y[16 * e + 2 * i + 1]);
-                    if (row < len) store32(o + 32 * x + 16 * e, u, wide);
-                }
-            }
-            give(&r_o);
-            if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
         }
     }
     tc::fence_before();
@@ -572,7 +562,7 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
         }
         wait(&ld[s], ph2);
         if (a.cu && len < kCT) zero_tail(X, P / 64, len, tid, kNT);
-        scale_hi_lo<N, kNT>(A, LOW, REV ? gates[s].er : gates[s].wt, len, tid);
+        scale_hi_lo<N, kNT, kCT>(A, LOW, REV ? gates[s].er : gates[s].wt, 0, len, tid);
         if (gt >= 0 && m + 1 < n_chunks) gates_of(m + 1);
         if (!LOCAL && warp == 0 && elect()) tc::bulk_wait_read();
         handoff();
@@ -668,7 +658,8 @@ cudaError_t fwd_np(const ScanArgs &a, cudaStream_t s) {
     ChainMaps cm;
     const int MB = a.cu ? 1 : a.B;
     if (!scan_tile_map(&m.q, a.q, a.ldq, MB, a.T, a.G, N) || !scan_tile_map(&m.k, a.k, a.ldk, MB, a.T, a.G, N) ||
-        !scan_tile_map(&m.v, a.v, a.ldv, MB, a.T, a.H, P))
+        !scan_tile_map(&m.v, a.v, a.ldv, MB, a.T, a.H, P) ||
+        (a.o && !scan_tile_map(&m.o, a.o, (long long)a.H * P, MB, a.T, a.H, P)))
         return cudaErrorInvalidValue;
     cudaError_t e;
     cm.a = m.k;

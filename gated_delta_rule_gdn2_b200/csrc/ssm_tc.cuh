@@ -266,16 +266,15 @@ __device__ __forceinline__ void zero_tail(unsigned char *tile, int nblk, int len
     }
 }
 
-// Rows of a [128][64 w] tile scaled by f[row], in two bf16 parts whose sum
-// carries 16 bits: the parts of the first go in place, of the rest to `lo`.
-// Rows from len on become zero whatever they hold.
-template <int D, int NT>
-__device__ __forceinline__ void scale_hi_lo(unsigned char *hi, unsigned char *lo, const float *f, int len, int tid) {
-    // eight consecutive lanes take the eight pieces of one 128-byte row; a
-    // thread's pieces lie NT / 8 rows apart, four loaded ahead of their use
-    constexpr int PER = kCT * (D / 8) / NT;
-    static_assert(PER % 4 == 0 || PER == 2, "pieces of a thread");
-    constexpr int U = PER % 4 == 0 ? 4 : 2;
+// Rows r0 .. r0 + ROWS - 1 of a [128][D] tile scaled by f[row], in two bf16
+// parts whose sum carries 16 bits: the parts of the first go in place, of the
+// rest to the [ROWS][D] tile `lo`.  Rows from len on become zero whatever they hold.
+template <int D, int NT, int ROWS>
+__device__ __forceinline__ void scale_hi_lo(unsigned char *hi, unsigned char *lo, const float *f, int r0, int len, int tid) {
+    // eight consecutive lanes take the eight pieces of one 128-byte row; up to
+    // four pieces of a thread are loaded ahead of their use
+    constexpr int PER = ROWS * (D / 8) / NT, U = PER % 4 == 0 ? 4 : 2;
+    static_assert(PER % U == 0 && ROWS % 8 == 0, "pieces of a thread");
     const bool whole = len == kCT;
 #pragma unroll 1
     for (int i0 = 0; i0 < PER; i0 += U) {
@@ -283,26 +282,26 @@ __device__ __forceinline__ void scale_hi_lo(unsigned char *hi, unsigned char *lo
         float w[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int id = tid + (i0 + i) * NT;
-            x[i] = *reinterpret_cast<const uint4 *>(hi + id * 16);
-            w[i] = f[(id / 8) % kCT];
+            const int id = tid + (i0 + i) * NT, blk = id / (ROWS * 8), r = r0 + (id / 8) % ROWS;
+            x[i] = *reinterpret_cast<const uint4 *>(hi + blk * (kCT * 128) + r * 128 + (id % 8) * 16);
+            w[i] = f[r];
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int id = tid + (i0 + i) * NT;
+            const int id = tid + (i0 + i) * NT, blk = id / (ROWS * 8), r = r0 + (id / 8) % ROWS;
             uint4 y;
             uint32_t *xe = reinterpret_cast<uint32_t *>(&x[i]), *ye = reinterpret_cast<uint32_t *>(&y);
             const float2 w2 = make_float2(w[i], w[i]);
-            const bool keep = whole || (id / 8) % kCT < len;
+            const bool keep = whole || r < len;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 v = unpack2(xe[e]), t = __fmul2_rn(v, w2);
                 const uint32_t h = pack2(t.x, t.y);
-                const float2 hf = unpack2(h), r = __ffma2_rn(hf, make_float2(-1.f, -1.f), t);
+                const float2 hf = unpack2(h), d = __ffma2_rn(hf, make_float2(-1.f, -1.f), t);
                 xe[e] = keep ? h : 0u;
-                ye[e] = keep ? pack2(r.x, r.y) : 0u;
+                ye[e] = keep ? pack2(d.x, d.y) : 0u;
             }
-            *reinterpret_cast<uint4 *>(hi + id * 16) = x[i];
+            *reinterpret_cast<uint4 *>(hi + blk * (kCT * 128) + r * 128 + (id % 8) * 16) = x[i];
             *reinterpret_cast<uint4 *>(lo + id * 16) = y;
         }
     }
