@@ -63,11 +63,11 @@ __device__ __forceinline__ void form_bwd_gates(BwdGates &g, float la, float dt, 
     if (t == 0) g.gamma = exp_ftz(b0 + b1 + b2 + b3);
 }
 
-// Sums over the 32 lanes of 16 values a lane: lanes 2 c and 2 c + 1 end with
-// the sum of value c (each step keeps the upper half where the lane's bit m is set).
-__device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
+// Sums over the 32 lanes of 8 values a lane: lanes 4 c .. 4 c + 3 end with the
+// sum of value c (each step keeps the upper half where the lane's bit m is set).
+__device__ __forceinline__ float lane_sums8(float (&v)[8], int lane) {
 #pragma unroll
-    for (int n = 8, m = 16; n >= 1; n >>= 1, m >>= 1) {
+    for (int n = 4, m = 16; n >= 1; n >>= 1, m >>= 1) {
         const bool up = lane & m;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -75,7 +75,8 @@ __device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
     }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+    const float s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return s + __shfl_xor_sync(0xffffffffu, s, 1);
 }
 
 template <int N>
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t ld_qk, ld[2], b_x, b_y, b_c, b_d, b_e, b_z;
     __shared__ uint32_t tmem_slot;
+    __shared__ int dead;
     BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
     float(*rowp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::ROWP), (*colp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::COLP);
     float(*rp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::RP), (*up)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::UP);
@@ -127,6 +129,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         uint64_t *bars[] = {&ld_qk, &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_e, &b_z};
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
         tc::fence_mbar_init();
+        dead = 0;
     }
     tc::fence_before();
     __syncthreads();
@@ -135,6 +138,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
 
     int nl = 0;
     auto load = [&](int u) {
+        ++nl;
+        if (!elect()) return;
         const int s = u & 1, h = h_lo + u / NX, x = u % NX;
         unsigned char *st = sm + L::ST0 + s * L::STAGE;
         tc::mbar_expect_tx(&ld[s], L::STAGE);
@@ -143,14 +148,11 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         const size_t img = ((size_t)slot * f.H + h) * (N * P * 2) + (size_t)x * L::SB;
         tc::bulk_load(st + 2 * L::VB, static_cast<const unsigned char *>(a.grads) + img, L::SB, &ld[s]);
         tc::bulk_load(st + 2 * L::VB + L::SB, static_cast<const unsigned char *>(f.states) + img, L::SB, &ld[s]);
-        ++nl;
     };
     bool bad = false, aborted = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!tc::mbar_wait(bar, parity)) {
-            bad = true;
-            record_status(f.status, GDN2_ERR_TIMEOUT);
-        }
+        if (!wait_bar(bar, parity, &dead)) bad = true;
+        __syncwarp();
     };
     auto handoff = [&]() {
         tc::fence_async_smem();
@@ -158,11 +160,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         aborted = __syncthreads_or(bad);
         tc::fence_after();
     };
-    if (tid == 0) {
-        tc::mbar_expect_tx(&ld_qk, 2 * L::QB);
-        for (int x = 0; x < N / 64; ++x) {
-            tc::tma_load_5d(sm + L::K + x * kCT * 128, &maps.k, 0, mt, x, g, mb, &ld_qk);
-            tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt, x, g, mb, &ld_qk);
+    if (warp == 0) {
+        if (elect()) {
+            tc::mbar_expect_tx(&ld_qk, 2 * L::QB);
+            for (int x = 0; x < N / 64; ++x) {
+                tc::tma_load_5d(sm + L::K + x * kCT * 128, &maps.k, 0, mt, x, g, mb, &ld_qk);
+                tc::tma_load_5d(sm + L::Q + x * kCT * 128, &maps.q, 0, mt, x, g, mb, &ld_qk);
+            }
         }
         if (nu > 0) load(0);
         if (nu > 1) load(1);
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         form_bwd_gates(gates[0], g_la, g_dt, gt);
         load_gates(1);
     }
-    for (int i = tid; i < 16 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp, colp, rp, up lie side by side)
+    for (int i = tid; i < 17 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp, colp, rp, up, cd lie side by side)
 
     // ---- G^T = k q^T, kept as bf16 pairs in tensor memory
     wait(&ld_qk, 0);
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         zero_tail(sm + L::Q, N / 64, len, tid, kNT);
     }
     handoff();
-    if (tid == 0) {
+    if (warp == 0 && elect()) {
         mma_tiles<true, true>(tm + cX, sm + L::K, kCT, sm + L::Q, kCT, N / 16, idX, false);
         tc::commit(&b_z);
     }
@@ -231,11 +235,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             handoff();
             if (aborted) break;
         }
-        if (tid == 0) {
-            mma_tiles<true, true>(tm + cX, sV, kCT, sO, kCT, 4, idX, false);
-            tc::commit(&b_x);
-            mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
-            tc::commit(&b_y);
+        if (warp == 0) {
+            if (elect()) {
+                mma_tiles<true, true>(tm + cX, sV, kCT, sO, kCT, 4, idX, false);
+                tc::commit(&b_x);
+                mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
+                tc::commit(&b_y);
+            }
             if (u > 0 && u + 1 < nu) {  // the other stage: free once its last product is done
                 wait(&b_e, (u - 1) & 1);
                 load(u + 1);
@@ -258,52 +264,59 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         tc::fence_after();
         // ---- X: token j = row, tokens i = 32 qc ..
         if (qc >= p) {
+            const bool dg = qc == p;  // the block on the diagonal
             const float lj = G.l[row];
-            const float fj = qc > p ? G.cf[row] * exp_ftz(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]) : 0.f;
-            float col = 0.f;
+            const float fj = dg ? 0.f : G.cf[row] * exp_ftz(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]);
+            const float *src = dg ? &G.l[32 * qc] : &G.lf[32 * qc];
+            float col = 0.f, diag = 0.f;
+            const float2 dt2 = make_float2(dtj, dtj);
+            // 8 columns at a time: beside Z and dq there is no room for more
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float X[16], w[16];
-                uint32_t gp[8];
-                ld16(tl + cX + 32 * qc + 16 * hf, X);
-                ld8(tl + cG + 16 * qc + 8 * hf, gp);
+            for (int c0 = 0; c0 < 32; c0 += 8) {
+                float X[8], c[8];
+                uint32_t gp[4];
+                *reinterpret_cast<float4 *>(&c[0]) = *reinterpret_cast<const float4 *>(src + c0);
+                *reinterpret_cast<float4 *>(&c[4]) = *reinterpret_cast<const float4 *>(src + c0 + 4);
+                ld8(tl + cX + 32 * qc + c0, X);
+                ld4(tl + cG + 16 * qc + c0 / 2, gp);
+                const int d = lane - c0;  // the diagonal's column
+                if (dg) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) c[i] = exp_ftz(i >= d ? c[i] - lj : -INFINITY);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) c[i] *= fj;
+                }
                 tc::wait_ld();
-                uint32_t am[8];
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float2 gg = unpack2(gp[i / 2]);
-                    float d0, d1;
-                    const int i0 = 16 * hf + i;  // within the block
-                    if (qc > p) {
-                        const float2 lf = *reinterpret_cast<const float2 *>(&G.lf[32 * qc + i0]);
-                        d0 = lf.x * fj;
-                        d1 = lf.y * fj;
-                    } else {
-                        const float2 l2 = *reinterpret_cast<const float2 *>(&G.l[32 * qc + i0]);
-                        d0 = i0 >= lane ? exp_ftz(l2.x - lj) : 0.f;
-                        d1 = i0 + 1 >= lane ? exp_ftz(l2.y - lj) : 0.f;
-                    }
-                    const float x0 = X[i] * d0, x1 = X[i + 1] * d1;
-                    Z[i0] = fmaf(x0, dtj, Z[i0]);
-                    Z[i0 + 1] = fmaf(x1, dtj, Z[i0 + 1]);
-                    am[i / 2] = pack2(gg.x * d0, gg.y * d1);
-                    float w0 = gg.x * x0, w1 = gg.y * x1;
-                    if (qc == p) {  // the diagonal apart: it is in ddt, not in dla
-                        if (i0 == lane) { cd[row] = x == 0 ? w0 : cd[row] + w0; w0 = 0.f; }
-                        if (i0 + 1 == lane) { cd[row] = x == 0 ? w1 : cd[row] + w1; w1 = 0.f; }
-                    }
-                    col += w0 + w1;
-                    w[i] = w0 * dtj;
-                    w[i + 1] = w1 * dtj;
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 gg = unpack2(gp[i / 2]), cc = make_float2(c[i], c[i + 1]);
+                    const float2 x2 = __fmul2_rn(make_float2(X[i], X[i + 1]), cc), m = __fmul2_rn(gg, cc), w = __fmul2_rn(gg, x2);
+                    const float2 z = __ffma2_rn(x2, dt2, make_float2(Z[c0 + i], Z[c0 + i + 1]));
+                    Z[c0 + i] = z.x;
+                    Z[c0 + i + 1] = z.y;
+                    gp[i / 2] = pack2(m.x, m.y);
+                    X[i] = w.x;
+                    X[i + 1] = w.y;
                 }
-                st8(tl + cA + 16 * qc + 8 * hf, am);
-                const float rs = lane_sums16(w, lane);
-                if ((lane & 1) == 0) {
-                    float *dst = &rowp[p][32 * qc + 16 * hf + (lane >> 1)];
-                    *dst = x == 0 ? rs : *dst + rs;
+                st4(tl + cA + 16 * qc + c0 / 2, gp);
+                if (dg) {  // the diagonal apart: it is in ddt, not in dla
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        diag += i == d ? X[i] : 0.f;
+                        X[i] = i == d ? 0.f : X[i];
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    col += X[i];
+                    X[i] *= dtj;
+                }
+                const float rs = lane_sums8(X, lane);
+                if ((lane & 3) == 0) rowp[p][32 * qc + c0 + (lane >> 2)] += rs;
             }
-            colp[qc][row] = x == 0 ? col : colp[qc][row] + col;
+            colp[qc][row] += col;
+            if (dg) cd[row] += diag;
         }
         // ---- Y: token j = row, value columns 16 qc ..
         wait(&b_y, ph);
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
             }
             stw<16>(tl + cY + 16 * qc, y);
-            rp[qc][row] = x == 0 ? r : rp[qc][row] + r;
+            rp[qc][row] += r;
             tc::wait_st();
         }
         if (x == NX - 1) {
@@ -348,10 +361,10 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             form_bwd_gates(gates[(hh + 1) & 1], g_la, g_dt, gt);
             load_gates(hh + 2);
         }
-        if (tid == 0) tc::bulk_wait_read();  // the dv tile of the unit before
+        if (warp == 0 && elect()) tc::bulk_wait_read();  // the dv tile of the unit before
         handoff();
         if (aborted) break;
-        if (tid == 0) {
+        if (warp == 0 && elect()) {
             const uint64_t o0 = tct::mnmaj(sO, kCT, 0);
 #pragma unroll
             for (int i = 0; i < kCT / 16; ++i)
@@ -408,11 +421,11 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 }
             }
             us *= er;
-            up[qc][row] = x == 0 ? us : up[qc][row] + us;
+            up[qc][row] += us;
         }
         handoff();
         if (aborted) break;
-        if (tid == 0 && !tail) {
+        if (warp == 0 && !tail && elect()) {
             tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
             tc::bulk_commit();
         }
@@ -424,19 +437,31 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         if (x == NX - 1 && warp == 3) {
             // dla_t = sum_{i >= t} (u_i + rowsum_i - dt_i colsum_i) + sum_{j < t} dt_j r_j + e^{L_end} <E, S>,
-            // ddt_t = r_t + colsum_t + the diagonal: four tokens a lane
-            float xs[4], ys[4], rr[4], cc[4], sx = 0.f, sy = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * lane + e;
-                const float row_s = (rowp[0][t] + rowp[1][t]) + (rowp[2][t] + rowp[3][t]);
-                cc[e] = (colp[0][t] + colp[1][t]) + (colp[2][t] + colp[3][t]);
-                rr[e] = (rp[0][t] + rp[1][t]) + (rp[2][t] + rp[3][t]);
-                xs[e] = (up[0][t] + up[1][t]) + (up[2][t] + up[3][t]) + row_s - G.dt[t] * cc[e];
-                ys[e] = G.dt[t] * rr[e];
-                sx += xs[e];
-                sy += ys[e];
-            }
+            // ddt_t = r_t + colsum_t + the diagonal: four tokens a lane.  The sums
+            // are read and left at zero for the next head.
+            auto take = [&](float(*part)[kCT], float4 &v) {
+                v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    float4 *src = reinterpret_cast<float4 *>(&part[i][4 * lane]);
+                    const float4 y = *src;
+                    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+                    *src = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            };
+            float4 ro, co, rr, uu;
+            take(rowp, ro);
+            take(colp, co);
+            take(rp, rr);
+            take(up, uu);
+            float4 *cdl = reinterpret_cast<float4 *>(&cd[4 * lane]);
+            const float4 di = *cdl, t4 = *reinterpret_cast<const float4 *>(&G.dt[4 * lane]);
+            *cdl = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float xs[4] = {uu.x + ro.x - t4.x * co.x, uu.y + ro.y - t4.y * co.y, uu.z + ro.z - t4.z * co.z,
+                                 uu.w + ro.w - t4.w * co.w};
+            const float ys[4] = {t4.x * rr.x, t4.y * rr.y, t4.z * rr.z, t4.w * rr.w};
+            const float ds[4] = {rr.x + co.x + di.x, rr.y + co.y + di.y, rr.z + co.z + di.z, rr.w + co.w + di.w};
+            float sx = (xs[0] + xs[1]) + (xs[2] + xs[3]), sy = (ys[0] + ys[1]) + (ys[2] + ys[3]);
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
                 const float px = __shfl_down_sync(0xffffffffu, sx, m), py = __shfl_up_sync(0xffffffffu, sy, m);
@@ -454,13 +479,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             run[2] = run[3] + xs[2];
             run[1] = run[2] + xs[1];
             run[0] = run[1] + xs[0];
+            bf16 *dla = static_cast<bf16 *>(a.dla) + (grow + 4 * lane) * f.H + h;
+            bf16 *ddt = static_cast<bf16 *>(a.ddt) + (grow + 4 * lane) * f.H + h;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int t = 4 * lane + e;
-                if (t < len) {
-                    const size_t r = (grow + t) * f.H + h;
-                    static_cast<bf16 *>(a.dla)[r] = __float2bfloat16_rn(run[e] + before + eall);
-                    static_cast<bf16 *>(a.ddt)[r] = __float2bfloat16_rn(rr[e] + cc[e] + cd[t]);
+                if (4 * lane + e < len) {
+                    dla[(size_t)e * f.H] = __float2bfloat16_rn(run[e] + before + eall);
+                    ddt[(size_t)e * f.H] = __float2bfloat16_rn(ds[e]);
                 }
                 before += ys[e];
             }
@@ -470,15 +495,11 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     // ---- dq += Z k, dk += Z^T q, and out
     if (!aborted && nu > 0) wait(&b_e, (nu - 1) & 1);
     if (!aborted) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(sm + L::ST0 + piece(kCT, row, 4 * qc + i)) =
-                make_uint4(pack2(Z[8 * i], Z[8 * i + 1]), pack2(Z[8 * i + 2], Z[8 * i + 3]), pack2(Z[8 * i + 4], Z[8 * i + 5]),
-                           pack2(Z[8 * i + 6], Z[8 * i + 7]));
+        put_row<32>(sm + L::ST0, kCT, row, 32 * qc, Z);
     }
     handoff();
     if (!aborted) {
-        if (tid == 0) {
+        if (warp == 0 && elect()) {
             mma_tiles<true, false>(tm + cDK, sm + L::ST0, kCT, sm + L::Q, kCT, kCT / 16, idZk, nu > 0);
             mma_tiles<false, false>(tm + cX, sm + L::ST0, kCT, sm + L::K, kCT, kCT / 16, idZq, false);
             tc::commit(&b_z);
@@ -511,17 +532,18 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             }
         }
     }
-    if (tid == 0) {  // nothing is left in flight
-        if (aborted) {
-            tc::commit(&b_z);
-            (void)tc::mbar_wait(&b_z, 1);
+    if (warp == 0) {  // nothing is left in flight
+        if (elect()) {
+            if (aborted) tc::commit(&b_z);
+            tc::bulk_wait();
         }
+        if (aborted) (void)tc::mbar_wait(&b_z, 1);
         if (nl > 0) (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
         if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
-        tc::bulk_wait();
     }
     tc::fence_before();
     __syncthreads();
+    if (tid == 0 && dead) record_status(f.status, GDN2_ERR_TIMEOUT);
     if (warp == 0) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);

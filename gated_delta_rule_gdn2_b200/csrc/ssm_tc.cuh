@@ -118,6 +118,16 @@ __device__ __forceinline__ void st8(uint32_t t, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(t), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
+__device__ __forceinline__ void ld8(uint32_t t, float (&v)[8]) { ld8(t, reinterpret_cast<uint32_t(&)[8]>(v)); }
+__device__ __forceinline__ void ld4(uint32_t t, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(t));
+}
+__device__ __forceinline__ void st4(uint32_t t, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]));
+}
 // 16 or 32 consecutive columns of this thread's lane
 template <int W>
 __device__ __forceinline__ void ldw(uint32_t t, float (&v)[W]) {
