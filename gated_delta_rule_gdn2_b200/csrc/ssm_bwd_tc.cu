@@ -9,13 +9,14 @@
 //     X = v dO^T            -> W = G D X: sums for dla and ddt; Z += D X dt
 //     Y = k E               -> r_j = w_j Y_j . v_j; Y scaled by w_j
 //     Y += (G D)^T dO       -> dv = dt Y + skip dO
-//     U = dO S^T            -> dq += e^L U (registers); u_i = e^{L_i} q_i . U_i
+//     dq += (e^L dO) S^T    -> u_i = q_i . (what it added)
 //     dk += (dt w v) E^T
 // and behind the last head dq += Z k, dk += Z^T q, so that both are summed over
 // the heads before they are rounded.  Rows of X, Y are tokens j (lanes of
 // tensor memory), columns i, so that (G D)^T is written back to tensor memory
 // as the left operand of the third product; the sums over j of W's columns are
-// a transposing reduction within each warp.  Operands rounded to bf16: G, G D,
+// a transposing reduction within each warp.  Operands rounded to bf16: G,
+// G D,
 // dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
 //
 // Bound: 64 KB in and 16 KB out a unit at dk = 128 against 1500 cycles of
@@ -28,6 +29,10 @@ namespace ssm {
 namespace {
 
 using tct::mma_tiles;
+
+// Warps 3 and 7 (last sub-partition, first token blocks) have no part in X:
+// one issues the copies and products, the other writes a head's dla and ddt.
+constexpr int kIssuer = 3, kFinisher = 7;
 
 struct BwdMaps {
     CUtensorMap q, k, v, dO, dv;
@@ -63,11 +68,11 @@ __device__ __forceinline__ void form_bwd_gates(BwdGates &g, float la, float dt, 
     if (t == 0) g.gamma = exp_ftz(b0 + b1 + b2 + b3);
 }
 
-// Sums over the 32 lanes of 8 values a lane: lanes 4 c .. 4 c + 3 end with the
-// sum of value c (each step keeps the upper half where the lane's bit m is set).
-__device__ __forceinline__ float lane_sums8(float (&v)[8], int lane) {
+// Sums over the 32 lanes of 16 values a lane: lanes 2 c and 2 c + 1 end with
+// the sum of value c (each step keeps the upper half where the lane's bit m is set).
+__device__ __forceinline__ float lane_sums16(float (&v)[16], int lane) {
 #pragma unroll
-    for (int n = 4, m = 16; n >= 1; n >>= 1, m >>= 1) {
+    for (int n = 8, m = 16; n >= 1; n >>= 1, m >>= 1) {
         const bool up = lane & m;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -75,8 +80,7 @@ __device__ __forceinline__ float lane_sums8(float (&v)[8], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
     }
-    const float s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 2);
-    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 template <int N>
@@ -84,16 +88,16 @@ struct BwdTcSmem {
     static constexpr int QB = kCT * N * 2, VB = kCT * 64 * 2, SB = N * 64 * 2, STAGE = 2 * VB + 2 * SB;
     static constexpr int K = 0, Q = QB, ST0 = 2 * QB, STG = ST0 + 2 * STAGE, G = STG + VB,
                          ROWP = G + 2 * (int)sizeof(BwdGates), COLP = ROWP + 4 * kCT * 4, RP = COLP + 4 * kCT * 4,
-                         UP = RP + 4 * kCT * 4, CD = UP + 4 * kCT * 4, RED = CD + kCT * 4, END = RED + 2 * 16 * 4;
+                         UP = RP + 4 * kCT * 4, CD = UP + 4 * kCT * 4, RED = CD + kCT * 4, FIN = RED + 2 * 16 * 4, END = FIN + 3 * kCT * 4;
     static constexpr int BYTES = END + 1024;
-    static_assert(BYTES + 128 <= 232448, "shared memory of an SM");
+    static_assert(BYTES + 1024 <= 232448, "shared memory of an SM");
 };
 
 template <int N, int P>
 __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid_constant__ BwdMaps maps) {
     using L = BwdTcSmem<N>;
     constexpr int NX = P / 64, WN = N / 4;  // units a head; a thread's columns of an N-column row
-    constexpr uint32_t cX = 0, cY = 128, cDK = 192, cA = 320, cG = 384;
+    constexpr uint32_t cX = 0, cDQ = 128, cY = 256, cDK = 320, cG = 448;  // ((G D)^T lies over X)
     constexpr uint32_t idX = tc::idesc_bf16(128, 128, false, false), idY = tc::idesc_bf16(128, 64, false, true),
                        idN = tc::idesc_bf16(128, N, false, false), idZk = tc::idesc_bf16(128, N, false, true),
                        idZq = tc::idesc_bf16(128, N, true, true);
@@ -105,7 +109,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
     float(*rowp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::ROWP), (*colp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::COLP);
     float(*rp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::RP), (*up)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::UP);
-    float *cd = reinterpret_cast<float *>(sm + L::CD), *red = reinterpret_cast<float *>(sm + L::RED);
+    float *cd = reinterpret_cast<float *>(sm + L::CD), *red = reinterpret_cast<float *>(sm + L::RED),
+          *fin = reinterpret_cast<float *>(sm + L::FIN);
     const ScanArgs &f = a.f;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, qc = warp >> 2, row = 32 * p + lane;
     const int hpg = f.H / f.G, per = (hpg + a.splits - 1) / a.splits;
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     const int mb = f.cu ? 0 : b, mt = (f.cu ? (int)sq.row0 : 0) + t0;
     const bool tail = f.cu && len < kCT;
 
-    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
         uint64_t *bars[] = {&ld_qk, &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_e, &b_z};
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         aborted = __syncthreads_or(bad);
         tc::fence_after();
     };
-    if (warp == 0) {
+    if (warp == kIssuer) {
         if (elect()) {
             tc::mbar_expect_tx(&ld_qk, 2 * L::QB);
             for (int x = 0; x < N / 64; ++x) {
@@ -171,9 +176,10 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         if (nu > 0) load(0);
         if (nu > 1) load(1);
     }
-    // the last four warps form the decay factors, one head ahead
+    // the warps of the last sub-partition, which have the least of X, form the
+    // decay factors, one head ahead
     float g_la = 0.f, g_dt = 0.f;
-    const int gt = tid - (kNT - kCT);
+    const int gt = p == 3 ? 32 * qc + lane : -1;
     auto load_gates = [&](int i) {
         g_la = g_dt = 0.f;
         if (i < nh && gt < len) {
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         zero_tail(sm + L::Q, N / 64, len, tid, kNT);
     }
     handoff();
-    if (warp == 0 && elect()) {
+    if (warp == kIssuer && elect()) {
         mma_tiles<true, true>(tm + cX, sm + L::K, kCT, sm + L::Q, kCT, N / 16, idX, false);
         tc::commit(&b_z);
     }
@@ -210,19 +216,53 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
 #pragma unroll
         for (int i = 0; i < 16; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
         st16(tl + cG + 16 * qc, u);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = 0u;
-        st16(tl + cA + 16 * qc, u);  // (blocks i < j of (G D)^T stay zero)
         tc::wait_st();
     }
     handoff();
 
-    float Z[32], dq[WN], es = 0.f, dsk = 0.f;
+    float Z[32], es = 0.f, dsk = 0.f, q_dq = 0.f;  // q_dq: q . dq so far
 #pragma unroll
     for (int i = 0; i < 32; ++i) Z[i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < WN; ++i) dq[i] = 0.f;
 
+    // dla_t = sum_{i >= t} (u_i + rowsum_i - dt_i colsum_i) + sum_{j < t} dt_j r_j + e^{L_end} <E, S>,
+    // ddt_t = r_t + colsum_t + the diagonal, of head h_lo + hh: one warp, four tokens a lane
+    float eall = 0.f, dall = 0.f;  // (kFinisher) e^{L_end} <E, S> and dskip's sum
+    auto finish = [&](int hh) {
+        const float4 x4 = *reinterpret_cast<const float4 *>(&fin[4 * lane]), y4 = *reinterpret_cast<const float4 *>(&fin[kCT + 4 * lane]);
+        const float4 d4 = *reinterpret_cast<const float4 *>(&fin[2 * kCT + 4 * lane]);
+        float sx = (x4.x + x4.y) + (x4.z + x4.w), sy = (y4.x + y4.y) + (y4.z + y4.w);
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float px = __shfl_down_sync(0xffffffffu, sx, m), py = __shfl_up_sync(0xffffffffu, sy, m);
+            if (lane + m < 32) sx += px;
+            if (lane >= m) sy += py;
+        }
+        if (lane == 0 && a.dskip_part) a.dskip_part[slot * f.H + h_lo + hh] = dall;
+        float after = __shfl_down_sync(0xffffffffu, sx, 1), before = __shfl_up_sync(0xffffffffu, sy, 1);
+        if (lane == 31) after = 0.f;
+        before = (lane == 0 ? 0.f : before) + eall;
+        const float r3 = after + x4.w, r2 = r3 + x4.z, r1 = r2 + x4.y, r0 = r1 + x4.x;
+        const float la[4] = {r0 + before, r1 + (before + y4.x), r2 + (before + y4.x + y4.y), r3 + (before + y4.x + y4.y + y4.z)};
+        const float dd[4] = {d4.x, d4.y, d4.z, d4.w};
+        const size_t at = (grow + 4 * lane) * f.H + h_lo + hh;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (4 * lane + e < len) {
+                static_cast<bf16 *>(a.dla)[at + (size_t)e * f.H] = __float2bfloat16_rn(la[e]);
+                static_cast<bf16 *>(a.ddt)[at + (size_t)e * f.H] = __float2bfloat16_rn(dd[e]);
+            }
+    };
+    // X of unit u (its stage has landed)
+    auto product_X = [&](int u) {
+        if (!elect()) return;
+        const unsigned char *v = sm + L::ST0 + (u & 1) * L::STAGE;
+        mma_tiles<true, true>(tm + cX, v, kCT, v + L::VB, kCT, 4, idX, false);
+        tc::commit(&b_x);
+    };
+    if (warp == kIssuer && nu > 0 && !tail) {
+        wait(&ld[0], 0);
+        product_X(0);
+    }
     for (int u = 0; u < nu && !aborted; ++u) {
         const int s = u & 1, hh = u / NX, x = u % NX, h = h_lo + hh;
         const uint32_t ph = u & 1, ph2 = (u >> 1) & 1;
@@ -235,10 +275,9 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             handoff();
             if (aborted) break;
         }
-        if (warp == 0) {
+        if (warp == kIssuer) {
+            if (tail) product_X(u);
             if (elect()) {
-                mma_tiles<true, true>(tm + cX, sV, kCT, sO, kCT, 4, idX, false);
-                tc::commit(&b_x);
                 mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
                 tc::commit(&b_y);
             }
@@ -248,48 +287,61 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             }
         }
         const float dtj = G.dt[row];
-        // <E, S> (the two images have one layout)
+        // <E, S> (the two images have one layout), by the warps with the least of X
+        if (p >= 2) {
+            const int t = (warp >> 2) * 64 + (p & 1) * 32 + lane;  // 0 .. 255
+#pragma unroll 2
+            for (int i = 0; i < L::SB / 16 / 256; ++i) {
+                const uint4 e = reinterpret_cast<const uint4 *>(sE)[t + i * 256], y4 = reinterpret_cast<const uint4 *>(sS)[t + i * 256];
+                const uint32_t ee[4] = {e.x, e.y, e.z, e.w}, tt[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
-        for (int i = 0; i < L::SB / 16 / kNT; ++i) {
-            const uint4 e = reinterpret_cast<const uint4 *>(sE)[tid + i * kNT], t = reinterpret_cast<const uint4 *>(sS)[tid + i * kNT];
-            const uint32_t ee[4] = {e.x, e.y, e.z, e.w}, tt[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 y = unpack2(ee[c]), z = unpack2(tt[c]);
-                es = fmaf(y.x, z.x, fmaf(y.y, z.y, es));
+                for (int c = 0; c < 4; ++c) {
+                    const float2 y = unpack2(ee[c]), z = unpack2(tt[c]);
+                    es = fmaf(y.x, z.x, fmaf(y.y, z.y, es));
+                }
             }
         }
-        if (u > 0 && x == 0) asm volatile("bar.sync 2, 512;\n" ::: "memory");  // the head before is summed up
+        if (u > 0 && x == 0) {  // the head before is summed up
+            asm volatile("bar.sync 2, 512;\n" ::: "memory");
+            if (warp == kFinisher) finish(hh - 1);  // (this warp has no part in X below)
+        }
         wait(&b_x, ph);
         tc::fence_after();
-        // ---- X: token j = row, tokens i = 32 qc ..
-        if (qc >= p) {
+        // ---- X: token j = row, tokens i = 32 qc ..; (G D)^T over the columns read
+        if (qc < p) {
+            const uint32_t z[16] = {0};
+            st16(tl + cX + 32 * qc, z);
+        } else {
             const bool dg = qc == p;  // the block on the diagonal
             const float lj = G.l[row];
             const float fj = dg ? 0.f : G.cf[row] * exp_ftz(qc - p == 1 ? 0.f : qc - p == 3 ? G.bs[1] + G.bs[2] : G.bs[p + 1]);
             const float *src = dg ? &G.l[32 * qc] : &G.lf[32 * qc];
-            float col = 0.f, diag = 0.f;
+            float2 col2 = make_float2(0.f, 0.f);
+            float diag = 0.f;
             const float2 dt2 = make_float2(dtj, dtj);
-            // 8 columns at a time: beside Z and dq there is no room for more
 #pragma unroll
-            for (int c0 = 0; c0 < 32; c0 += 8) {
-                float X[8], c[8];
-                uint32_t gp[4];
-                *reinterpret_cast<float4 *>(&c[0]) = *reinterpret_cast<const float4 *>(src + c0);
-                *reinterpret_cast<float4 *>(&c[4]) = *reinterpret_cast<const float4 *>(src + c0 + 4);
-                ld8(tl + cX + 32 * qc + c0, X);
-                ld4(tl + cG + 16 * qc + c0 / 2, gp);
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+                float X[16], c[16];
+                uint32_t gp[8];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(&c[i]) = *reinterpret_cast<const float4 *>(src + c0 + i);
+                ld16(tl + cX + 32 * qc + c0, X);
+                ld8(tl + cG + 16 * qc + c0 / 2, gp);
                 const int d = lane - c0;  // the diagonal's column
                 if (dg) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) c[i] = exp_ftz(i >= d ? c[i] - lj : -INFINITY);
+                    for (int i = 0; i < 16; ++i) c[i] = exp_ftz(i >= d ? c[i] - lj : -INFINITY);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) c[i] *= fj;
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 t = __fmul2_rn(make_float2(c[i], c[i + 1]), make_float2(fj, fj));
+                        c[i] = t.x;
+                        c[i + 1] = t.y;
+                    }
                 }
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
+                for (int i = 0; i < 16; i += 2) {
                     const float2 gg = unpack2(gp[i / 2]), cc = make_float2(c[i], c[i + 1]);
                     const float2 x2 = __fmul2_rn(make_float2(X[i], X[i + 1]), cc), m = __fmul2_rn(gg, cc), w = __fmul2_rn(gg, x2);
                     const float2 z = __ffma2_rn(x2, dt2, make_float2(Z[c0 + i], Z[c0 + i + 1]));
@@ -299,23 +351,25 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                     X[i] = w.x;
                     X[i + 1] = w.y;
                 }
-                st4(tl + cA + 16 * qc + c0 / 2, gp);
+                st8(tl + cX + 32 * qc + c0 / 2, gp);
                 if (dg) {  // the diagonal apart: it is in ddt, not in dla
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         diag += i == d ? X[i] : 0.f;
                         X[i] = i == d ? 0.f : X[i];
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    col += X[i];
-                    X[i] *= dtj;
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 w = make_float2(X[i], X[i + 1]), t = __fmul2_rn(w, dt2);
+                    col2 = __fadd2_rn(col2, w);
+                    X[i] = t.x;
+                    X[i + 1] = t.y;
                 }
-                const float rs = lane_sums8(X, lane);
-                if ((lane & 3) == 0) rowp[p][32 * qc + c0 + (lane >> 2)] += rs;
+                const float rs = lane_sums16(X, lane);
+                if ((lane & 1) == 0) rowp[p][32 * qc + c0 + (lane >> 1)] += rs;
             }
-            colp[qc][row] += col;
+            colp[qc][row] += col2.x + col2.y;
             if (dg) cd[row] += diag;
         }
         // ---- Y: token j = row, value columns 16 qc ..
@@ -324,7 +378,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         {
             float y[16];
             ld16(tl + cY + 16 * qc, y);
-            const float w = G.wt[row], wd = w * dtj;
+            const float w = G.wt[row], wd = w * dtj, er = G.er[row];
+            uint32_t eo[8];  // e^{L_i} dO_i, for dq: beside (G D)^T, over columns of X that this thread has read
             tc::wait_ld();
             float r = 0.f;
 #pragma unroll
@@ -342,10 +397,12 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                     y[c + 1] *= w;
                     r = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, r));
                     ve[e] = pack2(vv.x * wd, vv.y * wd);
+                    eo[4 * i + e] = pack2(oo.x * er, oo.y * er);
                 }
                 *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
             }
             stw<16>(tl + cY + 16 * qc, y);
+            st8(tl + cX + 32 * qc + 16, eo);
             rp[qc][row] += r;
             tc::wait_st();
         }
@@ -361,16 +418,19 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             form_bwd_gates(gates[(hh + 1) & 1], g_la, g_dt, gt);
             load_gates(hh + 2);
         }
-        if (warp == 0 && elect()) tc::bulk_wait_read();  // the dv tile of the unit before
+        if (warp == kIssuer && elect()) tc::bulk_wait_read();  // the dv tile of the unit before
         handoff();
         if (aborted) break;
-        if (warp == 0 && elect()) {
+        if (warp == kIssuer && elect()) {
             const uint64_t o0 = tct::mnmaj(sO, kCT, 0);
 #pragma unroll
             for (int i = 0; i < kCT / 16; ++i)
-                mma_ts(tm + cY, tm + cA + 8 * i, o0 + (tct::kstep_bytes<false>(kCT, i) >> 4), idY, true);
+                mma_ts(tm + cY, tm + cX + 32 * (i >> 1) + 8 * (i & 1), o0 + (tct::kstep_bytes<false>(kCT, i) >> 4), idY, true);
             tc::commit(&b_c);
-            mma_tiles<true, true>(tm + cX, sO, kCT, sS, N, 4, idN, false);
+            const uint64_t s0 = tct::kmaj(sS, N, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_ts(tm + cDQ, tm + cX + 32 * i + 16, s0 + (tct::kstep_bytes<true>(N, i) >> 4), idN, u > 0 || i > 0);
             tc::commit(&b_d);
             mma_tiles<true, true>(tm + cDK, sV, kCT, sE, N, 4, idN, u > 0);
             tc::commit(&b_e);
@@ -398,34 +458,34 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         wait(&b_d, ph);
         tc::fence_after();
-        {  // dq and u: token i = row, key channels WN qc ..
-            const float er = G.er[row];
+        {  // u_i = q_i . (what this unit added to dq_i): key channels WN qc ..
             float us = 0.f;
 #pragma unroll
             for (int hf = 0; hf < WN / 16; ++hf) {
                 float t[16];
-                ld16(tl + cX + WN * qc + 16 * hf, t);
+                ld16(tl + cDQ + WN * qc + 16 * hf, t);
+                uint32_t qe[8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4 *>(&qe[4 * i]) =
+                        *reinterpret_cast<const uint4 *>(sm + L::Q + piece(kCT, row, WN / 8 * qc + 2 * hf + i));
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(sm + L::Q + piece(kCT, row, WN / 8 * qc + 2 * hf + i));
-                    const uint32_t qe[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 qq = unpack2(qe[e]);
-                        const int c = 8 * i + 2 * e;
-                        us = fmaf(qq.x, t[c], fmaf(qq.y, t[c + 1], us));
-                        dq[16 * hf + c] = fmaf(er, t[c], dq[16 * hf + c]);
-                        dq[16 * hf + c + 1] = fmaf(er, t[c + 1], dq[16 * hf + c + 1]);
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    const float2 qq = unpack2(qe[e]);
+                    us = fmaf(qq.x, t[2 * e], fmaf(qq.y, t[2 * e + 1], us));
                 }
             }
-            us *= er;
-            up[qc][row] += us;
+            up[qc][row] += us - q_dq;
+            q_dq = us;
+        }
+        if (warp == kIssuer && !tail && u + 1 < nu) {  // the next X (the products that read (G D)^T and e^L dO are done)
+            wait(&ld[s ^ 1], (uint32_t)((u + 1) >> 1) & 1u);
+            product_X(u + 1);
         }
         handoff();
         if (aborted) break;
-        if (warp == 0 && !tail && elect()) {
+        if (warp == kIssuer && !tail && elect()) {
             tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
             tc::bulk_commit();
         }
@@ -435,62 +495,26 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 *reinterpret_cast<uint4 *>(dv + (size_t)(i / 8) * f.ldv + 8 * (i % 8)) =
                     *reinterpret_cast<const uint4 *>(sm + L::STG + piece(kCT, i / 8, i % 8));
         }
-        if (x == NX - 1 && warp == 3) {
-            // dla_t = sum_{i >= t} (u_i + rowsum_i - dt_i colsum_i) + sum_{j < t} dt_j r_j + e^{L_end} <E, S>,
-            // ddt_t = r_t + colsum_t + the diagonal: four tokens a lane.  The sums
-            // are read and left at zero for the next head.
-            auto take = [&](float(*part)[kCT], float4 &v) {
-                v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    float4 *src = reinterpret_cast<float4 *>(&part[i][4 * lane]);
-                    const float4 y = *src;
-                    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
-                    *src = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+        if (x == NX - 1 && p == 3) {  // the head's sums of token 32 qc + lane, left at zero for the next head
+            const int t = 32 * qc + lane;
+            auto take = [&](float(*part)[kCT]) {
+                const float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+                part[0][t] = part[1][t] = part[2][t] = part[3][t] = 0.f;
+                return v;
             };
-            float4 ro, co, rr, uu;
-            take(rowp, ro);
-            take(colp, co);
-            take(rp, rr);
-            take(up, uu);
-            float4 *cdl = reinterpret_cast<float4 *>(&cd[4 * lane]);
-            const float4 di = *cdl, t4 = *reinterpret_cast<const float4 *>(&G.dt[4 * lane]);
-            *cdl = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float xs[4] = {uu.x + ro.x - t4.x * co.x, uu.y + ro.y - t4.y * co.y, uu.z + ro.z - t4.z * co.z,
-                                 uu.w + ro.w - t4.w * co.w};
-            const float ys[4] = {t4.x * rr.x, t4.y * rr.y, t4.z * rr.z, t4.w * rr.w};
-            const float ds[4] = {rr.x + co.x + di.x, rr.y + co.y + di.y, rr.z + co.z + di.z, rr.w + co.w + di.w};
-            float sx = (xs[0] + xs[1]) + (xs[2] + xs[3]), sy = (ys[0] + ys[1]) + (ys[2] + ys[3]);
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const float px = __shfl_down_sync(0xffffffffu, sx, m), py = __shfl_up_sync(0xffffffffu, sy, m);
-                if (lane + m < 32) sx += px;
-                if (lane >= m) sy += py;
-            }
-            const float eall = warp_sum(lane < 16 ? red[lane] : 0.f) * G.gamma;
-            const float dall = warp_sum(lane < 16 ? red[16 + lane] : 0.f);
-            if (lane == 0 && a.dskip_part) a.dskip_part[slot * f.H + h] = dall;
-            float after = __shfl_down_sync(0xffffffffu, sx, 1), before = __shfl_up_sync(0xffffffffu, sy, 1);
-            if (lane == 31) after = 0.f;
-            if (lane == 0) before = 0.f;
-            float run[4];
-            run[3] = after + xs[3];
-            run[2] = run[3] + xs[2];
-            run[1] = run[2] + xs[1];
-            run[0] = run[1] + xs[0];
-            bf16 *dla = static_cast<bf16 *>(a.dla) + (grow + 4 * lane) * f.H + h;
-            bf16 *ddt = static_cast<bf16 *>(a.ddt) + (grow + 4 * lane) * f.H + h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (4 * lane + e < len) {
-                    dla[(size_t)e * f.H] = __float2bfloat16_rn(run[e] + before + eall);
-                    ddt[(size_t)e * f.H] = __float2bfloat16_rn(ds[e]);
-                }
-                before += ys[e];
+            const float ro = take(rowp), co = take(colp), r = take(rp), uu = take(up), dt = G.dt[t];
+            fin[t] = uu + ro - dt * co;
+            fin[kCT + t] = dt * r;
+            fin[2 * kCT + t] = r + co + cd[t];
+            cd[t] = 0.f;
+            if (warp == kFinisher) {
+                eall = warp_sum(lane < 16 ? red[lane] : 0.f) * G.gamma;
+                dall = warp_sum(lane < 16 ? red[16 + lane] : 0.f);
             }
         }
     }
+    __syncthreads();
+    if (!aborted && nu > 0 && warp == kFinisher) finish(nh - 1);
 
     // ---- dq += Z k, dk += Z^T q, and out
     if (!aborted && nu > 0) wait(&b_e, (nu - 1) & 1);
@@ -499,9 +523,9 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     }
     handoff();
     if (!aborted) {
-        if (warp == 0 && elect()) {
+        if (warp == kIssuer && elect()) {
             mma_tiles<true, false>(tm + cDK, sm + L::ST0, kCT, sm + L::Q, kCT, kCT / 16, idZk, nu > 0);
-            mma_tiles<false, false>(tm + cX, sm + L::ST0, kCT, sm + L::K, kCT, kCT / 16, idZq, false);
+            mma_tiles<false, false>(tm + cDQ, sm + L::ST0, kCT, sm + L::K, kCT, kCT / 16, idZq, nu > 0);
             tc::commit(&b_z);
         }
         wait(&b_z, 1);
@@ -510,11 +534,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             float t[WN];
-            ldw<WN>(tl + (which ? cDK : cX) + WN * qc, t);
+            ldw<WN>(tl + (which ? cDK : cDQ) + WN * qc, t);
             tc::wait_ld();
-            if (!which)
-#pragma unroll
-                for (int i = 0; i < WN; ++i) t[i] += dq[i];
             if (row < len) {
                 if (a.splits == 1) {
                     bf16 *dst = which ? static_cast<bf16 *>(a.dk) + (grow + row) * f.ldk + (size_t)g * N + WN * qc
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             }
         }
     }
-    if (warp == 0) {  // nothing is left in flight
+    if (warp == kIssuer) {  // nothing is left in flight
         if (elect()) {
             if (aborted) tc::commit(&b_z);
             tc::bulk_wait();
@@ -544,7 +565,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     tc::fence_before();
     __syncthreads();
     if (tid == 0 && dead) record_status(f.status, GDN2_ERR_TIMEOUT);
-    if (warp == 0) {
+    if (warp == kIssuer) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
     }
