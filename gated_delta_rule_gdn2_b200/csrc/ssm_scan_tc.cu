@@ -63,8 +63,6 @@ __device__ __forceinline__ void start_state(const float *first, const float *par
     }
 }
 
-__device__ __forceinline__ float token(const void *p, size_t i) { return __bfloat162float(static_cast<const bf16 *>(p)[i]); }
-
 // ---------------------------------------------------------------------------
 // Forward.  Four roles: warp 16 issues the copies and the products, warp 17
 // forms the decay factors up to four chunks ahead, and the other sixteen work
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     } else if (warp == 17) {
         for (int m = 0; m < n_chunks; ++m) {
             if (m >= kRing && !wait(&r_gfree[m % kRing], par(m - kRing, kRing))) break;
-            form_gates_warp(gates[m % kRing], a.la, a.dt, (size_t)sq.row0 * a.H + h, a.H, (c_lo + m) * kCT, sq.len, lane);
+            (void)form_gates_warp(gates[m % kRing], a.la, a.dt, (size_t)sq.row0 * a.H + h, a.H, (c_lo + m) * kCT, sq.len, lane, 0.f);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&r_gate[m % kRing]);
         }
@@ -438,23 +436,25 @@ struct ChainMaps {
 template <int N, int P, bool LOCAL>
 struct ChainSmem {
     static constexpr int AB = kCT * N * 2, XB = kCT * P * 2;
-    static constexpr int LO0 = 0, LO1 = LO0 + (LOCAL ? AB : 0), A0 = LO1 + AB, A1 = A0 + AB, X0 = A1 + AB, X1 = X0 + XB,
-                         S16 = X1 + XB, G = S16 + (LOCAL ? 0 : N * P * 2), END = G + 2 * (int)sizeof(Gates);
+    static constexpr int LO = 0, A = AB, X = A + 2 * AB, S16 = X + 2 * XB, G = S16 + (LOCAL ? 0 : N * P * 2),
+                         END = G + kRing * (int)sizeof(Gates);
     static constexpr int BYTES = END + 1024;
 };
 
+// Roles as in the forward: group A scales, group B (the chain only) keeps the
+// value's bf16 copy and decays it, one warp issues, one forms the factors.
 template <int N, int P, bool REV, bool LOCAL>
-__global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid_constant__ ChainMaps maps) {
+__global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, const __grid_constant__ ChainMaps maps) {
     using L = ChainSmem<N, P, LOCAL>;
-    constexpr int W = P / 4;
+    constexpr int HP = P / 2, IMG = N * P * 2;
     constexpr uint32_t idS = tc::idesc_bf16(128, P, true, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t ld[2], b_s[2], b_fin;
+    __shared__ uint64_t ld[2], d_s1, d_s, r_hl, r_hl2, r_st, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, qc = warp >> 2, row = 32 * p + lane;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, half = (warp >> 2) & 1, row = 32 * p + lane;
     const int np = LOCAL ? a.parts - 1 : a.parts;
     const int part = blockIdx.x % np + (LOCAL && REV ? 1 : 0), bh = blockIdx.x / np, b = bh / a.H, h = bh % a.H,
               g = h / (a.H / a.G);
@@ -469,10 +469,16 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
     auto chunk_of = [&](int m) { return DOWN ? c_hi - 1 - m : c_lo + m; };
     const int mb = a.cu ? 0 : b, mt = a.cu ? (int)sq.row0 : 0;
 
-    if (warp == 0) tc::tmem_alloc(&tmem_slot, 128);
+    if (warp == 16) tc::tmem_alloc(&tmem_slot, 128);
     if (tid == 0) {
-        uint64_t *bars[] = {&ld[0], &ld[1], &b_s[0], &b_s[1], &b_fin};
-        for (uint64_t *x : bars) tc::mbar_init(x, 1);
+        uint64_t *one[] = {&ld[0], &ld[1], &d_s1, &d_s, &d_fin};
+        for (uint64_t *x : one) tc::mbar_init(x, 1);
+        uint64_t *eight[] = {&r_hl, &r_hl2, &r_st};
+        for (uint64_t *x : eight) tc::mbar_init(x, 8);
+        for (int i = 0; i < kRing; ++i) {
+            tc::mbar_init(&r_gate[i], 1);
+            tc::mbar_init(&r_gfree[i], LOCAL ? 8 : 16);
+        }
         tc::fence_mbar_init();
         dead = 0;
     }
@@ -480,153 +486,145 @@ __global__ void __launch_bounds__(kNT, 1) chain_kernel(ChainArgs a, const __grid
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
-
-    int nl = 0;
-    auto load = [&](int m) {
-        ++nl;
-        if (!elect()) return;
-        const int s = m & 1, t = mt + chunk_of(m) * kCT;
-        tc::mbar_expect_tx(&ld[s], L::AB + L::XB);
-#pragma unroll
-        for (int x = 0; x < N / 64; ++x)
-            tc::tma_load_5d(sm + L::A0 + s * L::AB + x * kCT * 128, &maps.a, 0, t, x, g, mb, &ld[s]);
-#pragma unroll
-        for (int x = 0; x < P / 64; ++x)
-            tc::tma_load_5d(sm + L::X0 + s * L::XB + x * kCT * 128, &maps.x, 0, t, x, h, mb, &ld[s]);
-    };
-    bool bad = false, aborted = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!wait_bar(bar, parity, &dead)) bad = true;
-        __syncwarp();
-    };
-    auto handoff = [&]() {
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &dead)) != 0; };
+    auto give = [&](uint64_t *bar) {
         tc::fence_async_smem();
         tc::fence_before();
-        aborted = __syncthreads_or(bad);
-        tc::fence_after();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
     };
-    if (warp == 0) {
-        if (n_chunks > 0) load(0);
-        if (n_chunks > 1) load(1);
-    }
-    float g_la = 0.f, g_dt = 0.f, carry = 0.f;  // carry (LOCAL): the log decay of the chunks walked
-    const int gt = tid - (kNT - kCT);
-    auto load_gates = [&](int m) {
-        const int t = chunk_of(m) * kCT + gt;
-        g_la = g_dt = 0.f;
-        if (m < n_chunks && t < sq.len) {
-            const size_t r = (size_t)(sq.row0 + t) * a.H + h;
-            g_la = fmaxf(token(a.la, r), kLogMin);
-            g_dt = REV ? 1.f : token(a.dt, r);
-        }
-    };
-    // (REV weights e^{L_i}: er, with the carry where the walk is LOCAL)
-    auto gates_of = [&](int m) {
-        Gates &G = gates[m & 1];
-        form_gates(G, g_la, g_dt, gt, 1, LOCAL && !REV ? carry : 0.f);
-        if (LOCAL) {
-            if (REV) G.er[gt] *= exp_ftz(carry);
-            asm volatile("bar.sync 1, 128;\n" ::: "memory");
-            carry = fmaxf(carry + G.total, 2.f * kLogMin);  // (as good as -inf; kept finite)
-        }
-        load_gates(m + 1);
-    };
-    if (gt >= 0) {
-        load_gates(0);
-        gates_of(0);
-    }
-    float S[W];
-    constexpr int IMG = N * P * 2;
-    if (!LOCAL) {
-        start_state<N, P, W, REV>(a.first, a.part_state, a.part_decay, a.parts, part, bh, row, W * qc, S);
-        if (n_chunks > 0 && row < N) put_row<W>(sm + L::S16, N, row, W * qc, S);
-    }
-    __syncthreads();
-    if (!LOCAL && n_chunks > 0) {
-        const float gm = gates[0].gamma;
-        float t[W];
+    auto par = [](int m, int R) { return (uint32_t)(m / R) & 1u; };
+
+    if (warp == 16) {
+        if (n_chunks > 0) {
+            auto load = [&](int m) {
+                if (!elect()) return;
+                const int s = m & 1, t = mt + chunk_of(m) * kCT;
+                tc::mbar_expect_tx(&ld[s], L::AB + L::XB);
 #pragma unroll
-        for (int i = 0; i < W; ++i) t[i] = S[i] * gm;
-        stw<W>(tl + W * qc, t);
-        tc::wait_st();
-    }
-    handoff();
-    for (int m = 0; m < n_chunks; ++m) {
-        const int s = m & 1, len = min(kCT, sq.len - chunk_of(m) * kCT);
-        const uint32_t ph2 = (m >> 1) & 1;
-        unsigned char *A = sm + (s ? L::A1 : L::A0), *X = sm + (s ? L::X1 : L::X0),
-                      *LOW = sm + (LOCAL && s ? L::LO1 : L::LO0);
-        if (!LOCAL && warp == 0 && elect()) {
-            tc::bulk_store(a.images + ((size_t)(sq.slot + chunk_of(m)) * a.H + h) * IMG, sm + L::S16, IMG);
-            tc::bulk_commit();
-        }
-        wait(&ld[s], ph2);
-        if (a.cu && len < kCT) zero_tail(X, P / 64, len, tid, kNT);
-        scale_hi_lo<N, kNT, kCT>(A, LOW, REV ? gates[s].er : gates[s].wt, 0, len, tid);
-        if (gt >= 0 && m + 1 < n_chunks) gates_of(m + 1);
-        if (!LOCAL && warp == 0 && elect()) tc::bulk_wait_read();
-        handoff();
-        if (aborted) break;
-        if (warp == 0 && elect()) {
-            mma_tiles<false, false>(tm, A, kCT, X, kCT, kCT / 16, idS, !LOCAL || m > 0);
-            mma_tiles<false, false>(tm, LOW, kCT, X, kCT, kCT / 16, idS, true);
-            tc::commit(&b_s[s]);
-        }
-        if (LOCAL) {  // the product runs under the next chunk's scaling; its tiles are free when it is done
-            if (m > 0) {
-                wait(&b_s[s ^ 1], ((m - 1) >> 1) & 1);
-                if (warp == 0 && m + 1 < n_chunks) load(m + 1);
+                for (int x = 0; x < N / 64; ++x)
+                    tc::tma_load_5d(sm + L::A + s * L::AB + x * kCT * 128, &maps.a, 0, t, x, g, mb, &ld[s]);
+#pragma unroll
+                for (int x = 0; x < P / 64; ++x)
+                    tc::tma_load_5d(sm + L::X + s * L::XB + x * kCT * 128, &maps.x, 0, t, x, h, mb, &ld[s]);
+            };
+            auto product = [&](int m, int x, uint64_t *done) {
+                if (!elect()) return;
+                const unsigned char *k = sm + L::A + (m & 1) * L::AB + x * 64 * 128, *v = sm + L::X + (m & 1) * L::XB + x * 64 * 128;
+                mma_tiles<false, false>(tm, k, kCT, v, kCT, 4, idS, !LOCAL || m > 0 || x > 0);
+                mma_tiles<false, false>(tm, sm + L::LO + x * (L::AB / 2), 64, v, kCT, 4, idS, true);
+                if (!LOCAL && x) tc::bulk_wait_read();  // (S16's image has been read: the commit lets group B overwrite it)
+                tc::commit(done);
+            };
+            int nl = 1;  // loads issued
+            load(0);
+            if (n_chunks > 1) {
+                load(1);
+                nl = 2;
             }
-            continue;
+            for (int m = 0; m < n_chunks; ++m) {
+                const uint32_t ph = m & 1;
+                if (!wait(&r_hl, ph) || (!LOCAL && !wait(&r_st, ph))) break;
+                tc::fence_after();
+                if (!LOCAL && elect()) {
+                    tc::bulk_store(a.images + ((size_t)(sq.slot + chunk_of(m)) * a.H + h) * IMG, sm + L::S16, IMG);
+                    tc::bulk_commit();
+                }
+                __syncwarp();
+                product(m, 0, &d_s1);
+                if (!wait(&r_hl2, ph)) break;
+                tc::fence_after();
+                product(m, 1, &d_s);
+                if (m + 2 < n_chunks) {
+                    if (!wait(&d_s, ph)) break;
+                    load(m + 2);
+                    ++nl;
+                }
+            }
+            if (elect()) {  // nothing is left in flight
+                tc::commit(&d_fin);
+                tc::bulk_wait();
+            }
+            (void)tc::mbar_wait(&d_fin, 0);
+            (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
+            if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
         }
-        wait(&b_s[s], ph2);
-        tc::fence_after();
-        if (warp == 0 && m + 2 < n_chunks) load(m + 2);
-        ldw<W>(tl + W * qc, S);
-        tc::wait_ld();
-        if (m + 1 < n_chunks) {
-            if (row < N) put_row<W>(sm + L::S16, N, row, W * qc, S);
-            const float gm = gates[s ^ 1].gamma;
-            float t[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) t[i] = S[i] * gm;
-            stw<W>(tl + W * qc, t);
-            tc::wait_st();
+        __syncwarp();
+    } else if (warp == 17) {
+        float carry = 0.f;  // LOCAL: the log decay of the chunks walked
+        for (int m = 0; m < n_chunks; ++m) {
+            if (m >= kRing && !wait(&r_gfree[m % kRing], par(m - kRing, kRing))) break;
+            const float all = form_gates_warp(gates[m % kRing], a.la, REV ? nullptr : a.dt, (size_t)sq.row0 * a.H + h, a.H,
+                                              chunk_of(m) * kCT, sq.len, lane, carry);
+            if (LOCAL) carry = fmaxf(carry + all, 2.f * kLogMin);  // (as good as -inf; kept finite)
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&r_gate[m % kRing]);
         }
-        handoff();
-    }
-    if (LOCAL) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) S[i] = 0.f;
-        if (n_chunks > 0 && !aborted) {
-            wait(&b_s[(n_chunks - 1) & 1], ((n_chunks - 1) >> 1) & 1);
+        if (LOCAL && lane == 0)
+            a.part_decay[(size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)] = exp_ftz(carry);
+    } else if (warp < 8) {
+        for (int m = 0; m < n_chunks; ++m) {
+            const uint32_t ph = m & 1;
+            const int len = min(kCT, sq.len - chunk_of(m) * kCT);
+            const Gates &G = gates[m % kRing];
+            const float *f = REV ? G.er : G.wt;
+            unsigned char *A = sm + L::A + (m & 1) * L::AB;
+            if (!wait(&r_gate[m % kRing], par(m, kRing)) || !wait(&ld[m & 1], par(m, 2)) || (m > 0 && !wait(&d_s1, ph ^ 1))) break;
+            scale_hi_lo<N, 256, 64>(A, sm + L::LO, f, 0, len, tid);
+            if (a.cu && len < kCT) zero_tail(sm + L::X + (m & 1) * L::XB, P / 64, len, tid, 256);
+            give(&r_hl);
+            if (m > 0 && !wait(&d_s, ph ^ 1)) break;
+            scale_hi_lo<N, 256, 64>(A, sm + L::LO + L::AB / 2, f, 64, len, tid);
+            give(&r_hl2);
+            if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
+        }
+    } else {
+        // the value after chunk m - 1 (m = 0: the one that reaches this part): its
+        // bf16 copy, and decayed for chunk m; behind the last chunk, out
+        float *dst = nullptr;
+        if (LOCAL) dst = a.part_state + ((size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)) * N * P;
+        else if (part == (REV ? 0 : a.parts - 1) && a.last) dst = a.last + (size_t)bh * N * P;
+        for (int m = LOCAL ? n_chunks : 0; m <= n_chunks; ++m) {
+            const bool more = m < n_chunks;
+            // (LOCAL: the issuer's last commit, for this group has not followed the chunks' barrier)
+            if ((more && !wait(&r_gate[m % kRing], par(m, kRing))) ||
+                (m > 0 && !(LOCAL ? wait(&d_fin, 0) : wait(&d_s, (m - 1) & 1))))
+                break;
             tc::fence_after();
-            ldw<W>(tl + W * qc, S);
-            tc::wait_ld();
-        }
-    }
-    float *dst = nullptr;
-    if (LOCAL) dst = a.part_state + ((size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)) * N * P;
-    else if (part == (REV ? 0 : a.parts - 1) && a.last) dst = a.last + (size_t)bh * N * P;
-    if (dst && !aborted && row < N) {
-        dst += (size_t)row * P + W * qc;
+            const float gm = more ? gates[m % kRing].gamma : 0.f;
+#pragma unroll 1
+            for (int x = 0; x < HP / 32; ++x) {
+                const int c0 = HP * half + 32 * x;
+                float S[32];
+                if (m > 0) {
+                    tc::ld_32x32b_x32(tl + c0, S);
+                    tc::wait_ld();
+                } else {  // (LOCAL with no chunk: zero)
+                    start_state<N, P, 32, REV>(LOCAL ? nullptr : a.first, a.part_state, a.part_decay, LOCAL ? 1 : a.parts,
+                                               LOCAL ? 0 : part, bh, row, c0, S);
+                }
+                if (more) {
+                    if (row < N) put_row<32>(sm + L::S16, N, row, c0, S);
 #pragma unroll
-        for (int i = 0; i < W; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    }
-    if (LOCAL && gt == 0) a.part_decay[(size_t)bh * (a.parts - 1) + (REV ? part - 1 : part)] = exp_ftz(carry);
-    if (warp == 0) {  // nothing is left in flight
-        if (elect()) {
-            tc::commit(&b_fin);
-            tc::bulk_wait();
+                    for (int i = 0; i < 32; ++i) S[i] *= gm;
+                    tc::st_32x32b_x32(tl + c0, S);
+                } else if (dst && row < N) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4 *>(dst + (size_t)row * P + c0 + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                }
+            }
+            if (more) {
+                tc::wait_st();
+                give(&r_st);
+                if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
+            }
         }
-        (void)tc::mbar_wait(&b_fin, 0);
-        if (nl > 0) (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
-        if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
     }
     tc::fence_before();
     __syncthreads();
     if (tid == 0 && dead) record_status(a.status, GDN2_ERR_TIMEOUT);
-    if (warp == 0) {
+    if (warp == 16) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 128);
     }
@@ -643,7 +641,7 @@ cudaError_t go_chain(const ChainArgs &c, const ChainMaps &m, cudaStream_t s) {
     constexpr int bytes = ChainSmem<N, P, LOCAL>::BYTES;
     const cudaError_t e = big_smem(kernel, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(c.B * c.H * (LOCAL ? c.parts - 1 : c.parts)), kNT, bytes, s>>>(c, m);
+    kernel<<<(unsigned)(c.B * c.H * (LOCAL ? c.parts - 1 : c.parts)), kFwdThreads, bytes, s>>>(c, m);
     return cudaGetLastError();
 }
 

@@ -172,46 +172,20 @@ struct alignas(16) Gates {  // (read in 16-byte pieces, two side by side)
     float l[kCT], cf[kCT], er[kCT], wt[kCT], ld[kCT];
     float bs[4];    // the blocks' log decays
     float gamma;    // the chunk's decay
-    float total;    // its log
 };
-// Formed by four whole warps (t = 0..127 within them), with a named barrier
-// between the blocks' sums and what crosses blocks; `carry`: a log decay to add to wt's exponent.
-__device__ __forceinline__ void form_gates(Gates &g, float la, float dt, int t, int bar, float carry) {
-    const int lane = t & 31, w = t >> 5;
-    float up = la, dn = la;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, up, m), z = __shfl_down_sync(0xffffffffu, dn, m);
-        if (lane >= m) up += y;
-        if (lane + m < 32) dn += z;
-    }
-    const float behind = __shfl_down_sync(0xffffffffu, dn, 1), s = lane < 31 ? behind : 0.f;
-    g.l[t] = up;
-    g.cf[t] = exp_ftz(s) * dt;
-    if (lane == 31) g.bs[w] = up;
-    asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
-    const float b0 = g.bs[0], b1 = g.bs[1], b2 = g.bs[2], b3 = g.bs[3];
-    const float pre = w == 0 ? 0.f : w == 1 ? b0 : w == 2 ? b0 + b1 : b0 + b1 + b2;
-    const float post = w == 3 ? 0.f : w == 2 ? b3 : w == 1 ? b2 + b3 : b1 + b2 + b3;
-    g.er[t] = exp_ftz(pre + up);
-    g.wt[t] = exp_ftz(s + post + carry) * dt;
-    if (t == 0) {
-        const float all = b0 + b1 + b2 + b3;
-        g.gamma = exp_ftz(all);
-        g.total = all;
-    }
-}
-// The same by one warp, four tokens a lane, from token t0 of a sequence of len
-// tokens whose values lie `stride` elements apart from `first` on.
-__device__ __forceinline__ void form_gates_warp(Gates &g, const void *la, const void *dt, size_t first, int stride, int t0,
-                                                int len, int lane) {
+// Formed by one warp, four tokens a lane, from token t0 of a sequence of len
+// tokens whose values lie `stride` elements apart from `first` on (dt ==
+// nullptr: 1); `carry` is a log decay that er and wt hold besides.  Returns the
+// chunk's log decay.
+__device__ __forceinline__ float form_gates_warp(Gates &g, const void *la, const void *dt, size_t first, int stride, int t0,
+                                                 int len, int lane, float carry) {
     float x[4], d[4], up[4], dn[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int t = t0 + 4 * lane + e;
         const size_t r = first + (size_t)t * stride;
         x[e] = t < len ? fmaxf(__bfloat162float(static_cast<const bf16 *>(la)[r]), kLogMin) : 0.f;
-        d[e] = t < len ? __bfloat162float(static_cast<const bf16 *>(dt)[r]) : 0.f;
+        d[e] = t >= len ? 0.f : dt ? __bfloat162float(static_cast<const bf16 *>(dt)[r]) : 1.f;
     }
     up[0] = x[0];
     dn[3] = x[3];
@@ -242,8 +216,8 @@ __device__ __forceinline__ void form_gates_warp(Gates &g, const void *la, const 
         const float s = behind + (e < 3 ? dn[e + 1] : 0.f);
         l[e] = before + up[e];
         cf[e] = exp_ftz(s) * d[e];
-        er[e] = exp_ftz(pre + l[e]);
-        wt[e] = exp_ftz(s + post) * d[e];
+        er[e] = exp_ftz(pre + l[e] + carry);
+        wt[e] = exp_ftz(s + post + carry) * d[e];
     }
     *reinterpret_cast<float4 *>(&g.l[4 * lane]) = make_float4(l[0], l[1], l[2], l[3]);
     *reinterpret_cast<float4 *>(&g.cf[4 * lane]) = make_float4(cf[0], cf[1], cf[2], cf[3]);
@@ -253,10 +227,9 @@ __device__ __forceinline__ void form_gates_warp(Gates &g, const void *la, const 
     *reinterpret_cast<float4 *>(&g.ld[4 * lane]) =
         make_float4(l[0] - __logf(d[0]), l[1] - __logf(d[1]), l[2] - __logf(d[2]), l[3] - __logf(d[3]));
     if ((lane & 7) == 7) g.bs[w] = a;
-    if (lane == 0) {
-        g.total = b0 + b1 + b2 + b3;
-        g.gamma = exp_ftz(b0 + b1 + b2 + b3);
-    }
+    const float all = b0 + b1 + b2 + b3;
+    if (lane == 0) g.gamma = exp_ftz(all);
+    return all;
 }
 // log decay of the blocks strictly between block a and block b > a
 __device__ __forceinline__ float between(const Gates &g, int a, int b) {
