@@ -671,101 +671,105 @@ def chunk_fwd_gated(q, k, v, log_alpha, b, w, g, gamma, S0=None, output_final_st
 
 # --------------------------------------------------------------------------
 # selective state space scan and its prologue
+#
+# A single token's call is over in microseconds, so these checks are written to
+# cost little: shapes and strides are read once, and contiguous tensors take a
+# short way.
 
 
-class _On:
-    """The device of a call's tensors made current for it, and the stream it
-    runs on: the caller's, or the current one of that device.  Scratch that
-    the call allocates belongs to the device's current stream, so with a
-    stream of the caller's it is recorded there."""
-    __slots__ = ("guard", "stream", "given")
+def _elsewhere(t):
+    """Whether t's device is not the current one (the call is then made again
+    with it current: workspace sizes and launches go by the current device)."""
+    import torch
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("tensors must be CUDA tensors, got one on %s" % t.device)
+    return i != torch._C._cuda_getDevice()
 
-    def __init__(self, device, stream):
+
+def _raw_stream(t, stream):
+    if stream is None:
         import torch
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.given = stream
-        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-
-    def scratch(self, n, device):
-        """n bytes of workspace (None for none)."""
-        import torch
-        if not n:
-            return None
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if self.given is not None:
-            ws.record_stream(self.given if not isinstance(self.given, int)
-                             else torch.cuda.ExternalStream(self.given, device=device))
-        return ws
-
-    def done(self):
-        if self.guard is not None:
-            self.guard.__exit__(None, None, None)
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _row_ld(name, t, lead, width, strides_ok):
+def _scratch(n, like, stream):
+    """n bytes of workspace on like's device (None for none).  It belongs to
+    the current stream; for a call on another it is recorded there."""
+    import torch
+    if not n:
+        return None
+    ws = like.new_empty(n, dtype=torch.uint8)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
+    return ws
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_ld(name, t, lead, width):
     """Elements between the rows of t [*lead, *inner], whose inner dimensions
     are contiguous and whose leading ones are rows at one distance."""
-    n = len(lead)
-    if tuple(t.shape[:n]) != tuple(lead) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor with leading dimensions %s, got %s" % (name, tuple(lead), tuple(t.shape)))
-    st, sh = t.stride(), t.shape
-    inner, step = n, 1
+    if t.shape[:len(lead)] != lead:
+        raise ValueError("%s must have leading dimensions %s, got %s" % (name, tuple(lead), tuple(t.shape)))
+    if t.is_contiguous():
+        return width
+    n, st, sh = len(lead), t.stride(), t.shape
+    step = 1
     for d in range(t.dim() - 1, n - 1, -1):
         if sh[d] != 1 and st[d] != step:
             raise ValueError("%s must be contiguous within a row" % name)
         step *= sh[d]
-    # the row distance: that of the last leading dimension longer than one
-    ld = None
-    rows = 1
+    ld, rows = None, 1  # the distance is that of the last leading dimension longer than one
     for d in range(n - 1, -1, -1):
         if sh[d] != 1:
             if ld is None:
-                ld = st[d] if rows == 1 else None
-            if sh[d] > 1 and ld is not None and st[d] != ld * rows:
+                ld = st[d]
+            elif st[d] != ld * rows:
                 raise ValueError("%s must have its rows at one distance" % name)
         rows *= sh[d]
-    if ld is None or t.numel() == 0:
-        ld = width
-    if not strides_ok and ld != width:
-        raise ValueError("%s must be contiguous" % name)
-    return ld
+    return width if ld is None else ld
+
+
+def _check_like(name, t, shape, ref):
+    """A contiguous tensor of ref's dtype and device."""
+    if t.shape != shape or t.dtype != ref.dtype or t.get_device() != ref.get_device() or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, ref.dtype, tuple(shape), ref.device))
+
+
+def _check_f32(name, t, shape, ref):
+    import torch
+    if t is not None and (t.shape != shape or t.dtype != torch.float32 or t.get_device() != ref.get_device() or
+                          not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous fp32 tensor of shape %s on %s" % (name, tuple(shape), ref.device))
 
 
 def _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, lead_dims):
-    dtype = q.dtype
     if cu_seqlens is not None:
         lead_dims = 1
-    lead = tuple(v.shape[:lead_dims])
-    if v.dim() != lead_dims + 2 or q.dim() != lead_dims + 2:
+    vs, qs = v.shape, q.shape
+    if len(vs) != lead_dims + 2 or len(qs) != lead_dims + 2:
         raise ValueError("v must be %s + (H, dv) and q, k (G, dk)" % ("[rows]" if lead_dims == 1 else "[B, T]"))
-    H, dv = v.shape[-2:]
-    G, dk = q.shape[-2:]
-    for name, t in (("q", q), ("k", k), ("v", v), ("log_alpha", log_alpha), ("dt", dt)):
-        if t.dtype != dtype or t.device != q.device:
-            raise ValueError("%s must be a CUDA tensor of dtype %s on %s" % (name, dtype, q.device))
-    if tuple(k.shape) != tuple(q.shape) or G < 1 or H % G:
+    lead, (H, dv), (G, dk) = vs[:lead_dims], vs[-2:], qs[-2:]
+    dtype, dev = q.dtype, q.get_device()
+    if k.shape != qs or G < 1 or H % G:
         raise ValueError("q and k must share a shape [.., G, dk], G dividing H = %d" % H)
-    ldq, ldk, ldv = (_row_ld(n, t, lead, w, True) for n, t, w in (("q", q, G * dk), ("k", k, G * dk), ("v", v, H * dv)))
-    for name, t in (("log_alpha", log_alpha), ("dt", dt)):
-        if tuple(t.shape) != lead + (H,) or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous tensor of shape %s" % (name, lead + (H,)))
-    _check_f32("skip", skip, (H,), q.device)
+    if k.dtype != dtype or v.dtype != dtype or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k and v must be of one dtype and on one device")
+    ldq, ldk, ldv = _row_ld("q", q, lead, G * dk), _row_ld("k", k, lead, G * dk), _row_ld("v", v, lead, H * dv)
+    _check_like("log_alpha", log_alpha, lead + (H,), q)
+    _check_like("dt", dt, lead + (H,), q)
+    _check_f32("skip", skip, (H,), q)
     if cu_seqlens is None:
         B, T = (lead[0], 1) if lead_dims == 1 else lead
     else:
         B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
-        if cu_seqlens.device != q.device:
+        if cu_seqlens.get_device() != dev:
             raise ValueError("cu_seqlens must be on %s" % q.device)
     return lead, B, T, H, G, dk, dv, ldq, ldk, ldv
-
-
-def _check_f32(name, t, shape, device):
-    import torch
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
-                          t.device != device):
-        raise ValueError("%s must be a contiguous fp32 tensor of shape %s on %s" % (name, shape, device))
 
 
 def _like_rows(t, ld):
@@ -779,26 +783,27 @@ def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True,
     dt_t k_t v_t^T, o_t = S_t^T q_t + skip v_t.
 
     v [B, T, H, dv]; q, k [B, T, G, dk], each group read by H / G heads;
-    log_alpha, dt [B, T, H]; skip fp32 [H]; S0 fp32 [B, H, dk, dv].  q, k, v may
-    be views with a longer row stride.  Packed: [rows, ..] tensors and
-    cu_seqlens (B + 1 int32 offsets on the device).  With save_states=True
+    log_alpha <= 0 and dt >= 0 [B, T, H]; skip fp32 [H]; S0 fp32 [B, H, dk, dv].
+    q, k, v may be views with a longer row stride.  Packed: [rows, ..] tensors
+    and cu_seqlens (B + 1 int32 offsets on the device).  With save_states=True
     returns (o, S_T, states) for ssm_bwd(..., states=states)."""
     import torch
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return ssm_fwd(q, k, v, log_alpha, dt, skip, S0, output_final_state, save_states, cu_seqlens, stream)
     lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
-    code, dev, packed = _dtype_code(q), q.device, cu_seqlens is not None
-    _check_f32("S0", S0, (B, H, dk, dv), dev)
-    on = _On(dev, stream)
-    try:
-        o = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
-        S_T = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if output_final_state else None
-        states = None
-        if save_states:
-            states = torch.empty(gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed), dtype=torch.uint8, device=dev)
-        nws = gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, code, packed)
-        _raise(gdn2_ssm_fwd(q, k, v, log_alpha, dt, skip, S0, o, S_T, states, cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk,
-                            dv, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_fwd")
-    finally:
-        on.done()
+    code, packed = _dtype_code(q), cu_seqlens is not None
+    _check_f32("S0", S0, (B, H, dk, dv), q)
+    o = v.new_empty(lead + (H, dv))
+    S_T = v.new_empty((B, H, dk, dv), dtype=torch.float32) if output_final_state else None
+    states = None
+    if save_states:
+        states = v.new_empty(gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed), dtype=torch.uint8)
+    nws = load().gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, code, packed)
+    ws = _scratch(nws, q, stream)
+    _raise(load().gdn2_ssm_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
+                               _at(S0), o.data_ptr(), _at(S_T), _at(states), _at(cu_seqlens), ldq, ldk, ldv, B, T, H, G,
+                               dk, dv, code, _at(ws), nws, _raw_stream(q, stream)), "gdn2_ssm_fwd")
     return (o, S_T, states) if save_states else (o, S_T)
 
 
@@ -810,77 +815,77 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
     (dq, dk, dv) gives the tensors to write them to, such as views of the
     prologue's dy."""
     import torch
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return ssm_bwd(q, k, v, log_alpha, dt, dO, skip, S0, dS_T, states, need_dS0, cu_seqlens, into, stream)
     lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
-    code, dev, packed = _dtype_code(q), q.device, cu_seqlens is not None
-    _check_f32("S0", S0, (B, H, dk, dv), dev)
-    _check_f32("dS_T", dS_T, (B, H, dk, dv), dev)
-    if tuple(dO.shape) != lead + (H, dv) or dO.dtype != q.dtype or dO.device != dev or not dO.is_contiguous():
-        raise ValueError("dO must be a contiguous %s tensor of shape %s" % (q.dtype, lead + (H, dv)))
-    if states is not None and (states.dtype != torch.uint8 or states.device != dev or not states.is_contiguous() or
+    code, packed = _dtype_code(q), cu_seqlens is not None
+    _check_f32("S0", S0, (B, H, dk, dv), q)
+    _check_f32("dS_T", dS_T, (B, H, dk, dv), q)
+    _check_like("dO", dO, lead + (H, dv), q)
+    if states is not None and (states.dtype != torch.uint8 or states.get_device() != q.get_device() or
+                               not states.is_contiguous() or
                                states.numel() != gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed)):
         raise ValueError("states must be what ssm_fwd(..., save_states=True) returned for these sizes")
     for name, t, x, ld, w in zip(("dq", "dk", "dv"), into or (), (q, k, v), (ldq, ldk, ldv), (G * dk, G * dk, H * dv)):
-        if t.shape != x.shape or t.dtype != x.dtype or t.device != dev or _row_ld(name, t, lead, w, True) != ld:
+        if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device() or _row_ld(name, t, lead, w) != ld:
             raise ValueError("%s must have its input's shape, dtype and row stride" % name)
-    on = _On(dev, stream)
-    try:
-        dq, dk_, dv_ = into or (_like_rows(q, ldq), _like_rows(k, ldk), _like_rows(v, ldv))
-        g = {"dq": dq, "dk": dk_, "dv": dv_, "dlog_alpha": torch.empty_like(log_alpha),
-             "ddt": torch.empty_like(dt), "dskip": None if skip is None else torch.empty_like(skip),
-             "dS0": torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if need_dS0 else None}
-        nws = gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, code, packed, states is not None)
-        _raise(gdn2_ssm_bwd(q, k, v, log_alpha, dt, skip, S0, dO, dS_T, states, g["dq"], g["dk"], g["dv"],
-                            g["dlog_alpha"], g["ddt"], g["dskip"], g["dS0"], cu_seqlens, ldq, ldk, ldv, B, T, H, G, dk,
-                            dv, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_bwd")
-    finally:
-        on.done()
+    dq, dk_, dv_ = into or (_like_rows(q, ldq), _like_rows(k, ldk), _like_rows(v, ldv))
+    g = {"dq": dq, "dk": dk_, "dv": dv_, "dlog_alpha": torch.empty_like(log_alpha), "ddt": torch.empty_like(dt),
+         "dskip": None if skip is None else torch.empty_like(skip),
+         "dS0": q.new_empty((B, H, dk, dv), dtype=torch.float32) if need_dS0 else None}
+    nws = load().gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, code, packed, states is not None)
+    ws = _scratch(nws, q, stream)
+    _raise(load().gdn2_ssm_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
+                               _at(S0), dO.data_ptr(), _at(dS_T), _at(states), dq.data_ptr(), dk_.data_ptr(),
+                               dv_.data_ptr(), g["dlog_alpha"].data_ptr(), g["ddt"].data_ptr(), _at(g["dskip"]),
+                               _at(g["dS0"]), _at(cu_seqlens), ldq, ldk, ldv, B, T, H, G, dk, dv, code, _at(ws), nws,
+                               _raw_stream(q, stream)), "gdn2_ssm_bwd")
     return g
 
 
 def ssm_step(q, k, v, log_alpha, dt, S, skip=None, stream=None):
     """o = one token of the scan: v [B, H, dv], q, k [B, G, dk], log_alpha, dt
     [B, H]; S fp32 [B, H, dk, dv] updated in place."""
-    import torch
+    if _elsewhere(q):
+        import torch
+        with torch.cuda.device(q.device):
+            return ssm_step(q, k, v, log_alpha, dt, S, skip, stream)
     lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, None, 1)
-    dev = q.device
-    _check_f32("S", S, (B, H, dk, dv), dev)
-    on = _On(dev, stream)
-    try:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-        _raise(gdn2_ssm_step(q, k, v, log_alpha, dt, skip, S, o, ldq, ldk, ldv, B, H, G, dk, dv, _dtype_code(q),
-                             on.stream), "gdn2_ssm_step")
-    finally:
-        on.done()
+    _check_f32("S", S, (B, H, dk, dv), q)
+    o = v.new_empty((B, H, dv))
+    _raise(load().gdn2_ssm_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
+                                S.data_ptr(), o.data_ptr(), ldq, ldk, ldv, B, H, G, dk, dv, _dtype_code(q),
+                                _raw_stream(q, stream)), "gdn2_ssm_step")
     return o
 
 
 def _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, cu_seqlens, lead_dims):
-    dev = x.device
     if cu_seqlens is not None:
         lead_dims = 1
-    lead, C, K = tuple(x.shape[:lead_dims]), x.shape[-1], W.shape[-1]
-    if x.dim() != lead_dims + 1:
-        raise ValueError("x must be %s" % ("[rows, C]" if lead_dims == 1 else "[B, T, C]"))
-    _check_f32("W", W, (C, K), dev)
-    _check_f32("bias", bias, (C,), dev)
+    xs = x.shape
+    if len(xs) != lead_dims + 1 or W.dim() != 2:
+        raise ValueError("x must be %s and W [C, K]" % ("[rows, C]" if lead_dims == 1 else "[B, T, C]"))
+    lead, C, K = xs[:lead_dims], xs[-1], W.shape[1]
+    _check_f32("W", W, (C, K), x)
+    _check_f32("bias", bias, (C,), x)
     H, ldt = 0, 0
     if xdt is not None:
         H = xdt.shape[-1]
-        if xdt.dtype != x.dtype or xdt.device != dev or xdt.dim() != lead_dims + 1 or A_log is None:
-            raise ValueError("xdt must be a %s tensor %s + (H,) on %s, with A_log" % (x.dtype, lead, dev))
-        ldt = _row_ld("xdt", xdt, lead, H, True)
-        _check_f32("dt_bias", dt_bias, (H,), dev)
-        _check_f32("A_log", A_log, (H,), dev)
+        if xdt.dtype != x.dtype or xdt.get_device() != x.get_device() or xdt.dim() != lead_dims + 1 or A_log is None:
+            raise ValueError("xdt must be a %s tensor %s + (H,) on %s, with A_log" % (x.dtype, tuple(lead), x.device))
+        ldt = _row_ld("xdt", xdt, lead, H)
+        _check_f32("dt_bias", dt_bias, (H,), x)
+        _check_f32("A_log", A_log, (H,), x)
     if cu_seqlens is None:
         B, T = (lead[0], 1) if lead_dims == 1 else lead
     else:
         B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
-        if cu_seqlens.device != dev:
-            raise ValueError("cu_seqlens must be on %s" % dev)
-    if window is not None and (tuple(window.shape) != (B, K - 1, C) or window.dtype != x.dtype or
-                               window.device != dev or not window.is_contiguous()):
-        raise ValueError("the window must be a contiguous %s tensor of shape %s" % (x.dtype, (B, K - 1, C)))
-    return lead, B, T, C, K, H, _row_ld("x", x, lead, C, True), ldt
+        if cu_seqlens.get_device() != x.get_device():
+            raise ValueError("cu_seqlens must be on %s" % x.device)
+    if window is not None:
+        _check_like("the window", window, (B, K - 1, C), x)
+    return lead, B, T, C, K, H, _row_ld("x", x, lead, C), ldt
 
 
 def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False, cu_seqlens=None, stream=None):
@@ -888,21 +893,19 @@ def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False
     filters W fp32 [C, K], dt = softplus(xdt + dt_bias) and log_alpha =
     -exp(A_log) dt [B, T, H] (xdt None: neither).  init [B, K-1, C]: the inputs
     before each sequence (None: zeros); window: those before its next token
-    (None without output_window).  Packed: [rows, ..] and cu_seqlens."""
-    import torch
+    (None without output_window).  x and xdt may be slices of wider rows.
+    Packed: [rows, ..] and cu_seqlens."""
+    if _elsewhere(x):
+        import torch
+        with torch.cuda.device(x.device):
+            return ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init, output_window, cu_seqlens, stream)
     lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
-    code, dev = _dtype_code(x), x.device
-    on = _On(dev, stream)
-    try:
-        y = torch.empty(lead + (C,), dtype=x.dtype, device=dev)
-        dt = la = None
-        if H:
-            dt, la = (torch.empty(lead + (H,), dtype=x.dtype, device=dev) for _ in range(2))
-        window = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if output_window else None
-        _raise(gdn2_ssm_prologue_fwd(x, W, bias, K, xdt, dt_bias, A_log, init, y, dt, la, window, cu_seqlens, ldx, ldt,
-                                     B, T, C, H, code, on.stream), "gdn2_ssm_prologue_fwd")
-    finally:
-        on.done()
+    y = x.new_empty(lead + (C,))
+    dt, la = (x.new_empty(lead + (H,)), x.new_empty(lead + (H,))) if H else (None, None)
+    window = x.new_empty((B, K - 1, C)) if output_window else None
+    _raise(load().gdn2_ssm_prologue_fwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
+                                        _at(init), y.data_ptr(), _at(dt), _at(la), _at(window), _at(cu_seqlens), ldx, ldt,
+                                        B, T, C, H, _dtype_code(x), _raw_stream(x, stream)), "gdn2_ssm_prologue_fwd")
     return y, dt, la, window
 
 
@@ -911,42 +914,40 @@ def ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt=None, dlog_alpha=N
     """Gradients of ssm_prologue from dy, ddt and dlog_alpha: dx, dW, dbias,
     dxdt, ddt_bias, dA_log and, with init, dinit (None for what was not given)."""
     import torch
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt, dlog_alpha, init, cu_seqlens, stream)
     lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
-    code, dev = _dtype_code(x), x.device
     for name, t, w in (("dy", dy, C), ("ddt", ddt, H), ("dlog_alpha", dlog_alpha, H)):
-        if w and (t is None or tuple(t.shape) != lead + (w,) or t.dtype != x.dtype or t.device != dev or
-                  not t.is_contiguous()):
-            raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, x.dtype, lead + (w,)))
-    on = _On(dev, stream)
-    try:
-        g = {"dx": torch.empty(lead + (C,), dtype=x.dtype, device=dev), "dW": torch.empty_like(W)}
-        g.update({n: None if t is None else torch.empty_like(t) for n, t in (("dbias", bias), ("dinit", init))})
-        g.update({n: None if t is None or not H else torch.empty_like(t) for n, t in
-                  (("ddt_bias", dt_bias), ("dA_log", A_log))})
-        g["dxdt"] = torch.empty(lead + (H,), dtype=x.dtype, device=dev) if H else None
-        nws = gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, cu_seqlens is not None)
-        _raise(gdn2_ssm_prologue_bwd(x, W, bias, K, xdt, dt_bias, A_log, init, dy, ddt, dlog_alpha, g["dx"], g["dW"],
-                                     g["dbias"], g["dxdt"], g["ddt_bias"], g["dA_log"], g["dinit"], cu_seqlens, ldx, ldt,
-                                     B, T, C, H, code, on.scratch(nws, dev), nws, on.stream), "gdn2_ssm_prologue_bwd")
-    finally:
-        on.done()
+        if w:
+            if t is None:
+                raise ValueError("%s is missing" % name)
+            _check_like(name, t, lead + (w,), x)
+    e = torch.empty_like
+    g = {"dx": x.new_empty(lead + (C,)), "dW": e(W), "dbias": None if bias is None else e(bias),
+         "dinit": None if init is None else e(init), "ddt_bias": e(dt_bias) if H and dt_bias is not None else None,
+         "dA_log": e(A_log) if H else None, "dxdt": x.new_empty(lead + (H,)) if H else None}
+    nws = load().gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, cu_seqlens is not None)
+    ws = _scratch(nws, x, stream)
+    _raise(load().gdn2_ssm_prologue_bwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
+                                        _at(init), dy.data_ptr(), _at(ddt), _at(dlog_alpha), g["dx"].data_ptr(),
+                                        g["dW"].data_ptr(), _at(g["dbias"]), _at(g["dxdt"]), _at(g["ddt_bias"]),
+                                        _at(g["dA_log"]), _at(g["dinit"]), _at(cu_seqlens), ldx, ldt, B, T, C, H,
+                                        _dtype_code(x), _at(ws), nws, _raw_stream(x, stream)), "gdn2_ssm_prologue_bwd")
     return g
 
 
 def ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream=None):
     """(y, dt, log_alpha) of one token per sequence: x [B, C], xdt [B, H]
     (None: only y); window [B, K-1, C] updated in place."""
-    import torch
+    if _elsewhere(x):
+        import torch
+        with torch.cuda.device(x.device):
+            return ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream)
     lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, None, 1)
-    dev = x.device
-    on = _On(dev, stream)
-    try:
-        y = torch.empty((B, C), dtype=x.dtype, device=dev)
-        dt = la = None
-        if H:
-            dt, la = (torch.empty((B, H), dtype=x.dtype, device=dev) for _ in range(2))
-        _raise(gdn2_ssm_prologue_step(x, W, bias, K, xdt, dt_bias, A_log, window, y, dt, la, ldx, ldt, B, C, H,
-                                      _dtype_code(x), on.stream), "gdn2_ssm_prologue_step")
-    finally:
-        on.done()
+    y = x.new_empty((B, C))
+    dt, la = (x.new_empty((B, H)), x.new_empty((B, H))) if H else (None, None)
+    _raise(load().gdn2_ssm_prologue_step(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
+                                         _at(window), y.data_ptr(), _at(dt), _at(la), ldx, ldt, B, C, H, _dtype_code(x),
+                                         _raw_stream(x, stream)), "gdn2_ssm_prologue_step")
     return y, dt, la

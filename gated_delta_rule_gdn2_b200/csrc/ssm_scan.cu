@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(128) rec_kernel(RecArgs a) {
         }
         for (int x = 0; x < n; ++x) {
             const int t = REV ? n - 1 - x : x;
-            const float la = s_a[st][t], al = __expf(la), dt = s_d[st][t];
+            const float la = s_a[st][t], al = expf(la), dt = s_d[st][t];
             const float2 a2 = make_float2(al, al);
             const float4 v = *reinterpret_cast<const float4 *>(&s_v[st][t][warp * 16 + pg * 4]);
             const float2 v0 = make_float2(v.x * dt, v.y * dt), v1 = make_float2(v.z * dt, v.w * dt);
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
                     const int i = ti + 16 * r, j = tj + 16 * c;
                     // (r, c: the blocks of i and j)
                     const float mid = r == 2 && c == 0 ? b1 : r == 3 && c == 1 ? b2 : r == 3 && c == 0 ? b1 + b2 : 0.f;
-                    const float D = r > c ? __expf(lam[i] + mid + lsu[j]) : r == c && i >= j ? __expf(lam[i] - lam[j]) : 0.f;
+                    const float D = r > c ? expf(lam[i] + mid + lsu[j]) : r == c && i >= j ? expf(lam[i] - lam[j]) : 0.f;
                     const float x = X[r][c] * D, dtj = sdt[j], w = G[r][c] * x;
                     sM[i * L::LG + j] = G[r][c] * D;
                     Z[r][c] = fmaf(x, dtj, Z[r][c]);
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int j = ti + 16 * r;
-                const float w = __expf(lsu[j] + post[r]);
+                const float w = expf(lsu[j] + post[r]);
                 float d = 0.f;
 #pragma unroll
                 for (int u = 0; u < P / 64; ++u) {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int j = ti + 16 * r;
-                const float w = sdt[j] * __expf(lsu[j] + post[r]);
+                const float w = sdt[j] * expf(lsu[j] + post[r]);
 #pragma unroll
                 for (int c = 0; c < N / 16; ++c) dk[r][c] = fmaf(w, acc[r][c], dk[r][c]);
             }
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = ti + 16 * r;
-                const float w = __expf(pre[r] + lam[i]);
+                const float w = expf(pre[r] + lam[i]);
                 float d = 0.f;
 #pragma unroll
                 for (int u = 0; u < N / 64; ++u) {
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
             // lane l takes tokens 2 l, 2 l + 1
             float es_all = 0.f;
             for (int w = 0; w < 8; ++w) es_all += red[8 + w];
-            es_all *= __expf(Lend);
+            es_all *= expf(Lend);
             float col[2], x[2], y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
