@@ -5,8 +5,8 @@
 // A CTA of 16 warps takes one (sequence, head) -- or one part of it -- and
 // walks its chunks of 128 tokens with the fp32 state S [dk][dv] in tensor
 // memory.  In a chunk, with L_i the log decay from its start through token i,
-//     o_i = e^{L_i} S^T q_i + sum_{j <= i} M_ij v_j,
-//     M_ij = (q_i . k_j) e^{L_i - L_j} dt_j (+ skip where i = j),
+//     o_i = e^{L_i} S^T q_i + sum_{j <= i} M_ij v_j + skip v_i,
+//     M_ij = (q_i . k_j) e^{L_i - L_j} dt_j,
 //     S  <- e^{L_end} S + sum_j e^{L_end - L_j} dt_j k_j v_j^T,
 // as four products: G = q k^T; q S (S rounded to bf16); M v, with M = G masked,
 // decayed and rounded to bf16, written back to tensor memory as the left
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     // tiles landed; products done; hand-overs of the groups (one arrival a warp)
-    __shared__ uint64_t ld_qk[2], ld_v, d_g, d_yi, d_s1, d_s, d_y, r_hl, r_hl2, r_m, r_st, r_o, r_tail, r_gate[kRing], r_gfree[kRing], d_fin;
+    __shared__ uint64_t ld_qk[2], ld_v, d_g, d_yi, d_s1, d_s, d_y, r_hl, r_hl2, r_m, r_st, r_o, r_y2, r_tail, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     if (tid == 0) {
         uint64_t *one[] = {&ld_qk[0], &ld_qk[1], &ld_v, &d_g, &d_yi, &d_s1, &d_s, &d_y, &d_fin};
         for (uint64_t *x : one) tc::mbar_init(x, 1);
-        uint64_t *eight[] = {&r_hl, &r_hl2, &r_m, &r_st, &r_o, &r_tail};
+        uint64_t *eight[] = {&r_hl, &r_hl2, &r_m, &r_st, &r_o, &r_y2, &r_tail};
         for (uint64_t *x : eight) tc::mbar_init(x, 8);
         for (int i = 0; i < kRing; ++i) {
             tc::mbar_init(&r_gate[i], 1);
@@ -207,13 +207,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                     __syncwarp();
                     load_qk(m + 1);
                 }
-                if (!(ok = wait(&r_m, ph))) break;
+                if (!(ok = wait(&r_m, ph) && wait(&r_y2, ph))) break;
                 tc::fence_after();
                 if (elect()) {
                     const uint64_t v0 = tct::mnmaj(sm + L::V, kCT, 0);
 #pragma unroll
                     for (int x = 0; x < kCT / 16; ++x)
-                        mma_ts(tm + cY2, tm + cG + 8 * x + (x < 4 ? 0 : 32), v0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, x > 0);
+                        mma_ts(tm + cY2, tm + cG + 8 * x + (x < 4 ? 0 : 32), v0 + (tct::kstep_bytes<false>(kCT, x) >> 4), idY, true);
                     tc::commit(&d_y);
                 }
                 if (!(ok = wait(&r_hl2, ph))) break;
@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
         }
     } else if (warp < 8) {
         const int gt = tid;  // 0 .. 255
-        const float skip = a.skip ? a.skip[h] : 0.f;
         for (int m = 0; m < n_chunks; ++m) {
             const uint32_t ph = m & 1;
             const int len = min(kCT, sq.len - (c_lo + m) * kCT);
@@ -267,8 +266,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 zero_tail(sm + L::V, P / 64, len, gt, 256);
             }
             give(&r_hl);
-            // M = G masked and decayed, skip on its diagonal: row i = row,
-            // columns 64 half .., written over the columns of G that this thread
+            // M = G masked and decayed: row i = row, columns 64 half .., written over the columns of G that this thread
             // has read (64 half + 0 .. 31).  (Column factors are fetched whole before the
             // tile's values: a shared load takes hundreds of cycles while the
             // products stream their operands.)
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float e = exp_ftz(i <= d ? li - c[i] : -INFINITY);
-                        x[i] = fmaf(i <= d ? x[i] : 0.f, e, i == d ? skip : 0.f);
+                        x[i] = i <= d ? x[i] * e : 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = pack2(x[2 * i], x[2 * i + 1]);
@@ -335,8 +333,36 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 tc::st_32x32b_x32(tl + cS + c0, S);
             }
         }
+        // M v is added to skip v in fp32 (as part of M's diagonal the term would
+        // be rounded to bf16 once more: o's error 1.8e-3 -> 2.3e-3)
+        const float skip = a.skip ? a.skip[h] : 0.f;
+        auto start_y2 = [&]() {
+#pragma unroll 1
+            for (int x = 0; x < HP / 16; ++x) {
+                const int c0 = HP * half + 16 * x;
+                float y[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sm + L::V + piece(kCT, row, c0 / 8 + i));
+                    const uint32_t ve[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2(ve[e]);
+                        y[8 * i + 2 * e] = skip * f.x;
+                        y[8 * i + 2 * e + 1] = skip * f.y;
+                    }
+                }
+                stw<16>(tl + cY2 + c0, y);
+            }
+            tc::wait_st();
+        };
         tc::wait_st();
-        if (n_chunks > 0) give(&r_st);
+        if (n_chunks > 0) {
+            give(&r_st);
+            ok = ok && wait(&ld_v, 0);
+            if (ok) start_y2();
+            give(&r_y2);
+        }
         for (int m = 0; ok && m < n_chunks; ++m) {
             const uint32_t ph = m & 1;
             const int len = min(kCT, sq.len - (c_lo + m) * kCT);
@@ -386,6 +412,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 }
                 tc::wait_st();
                 give(&r_st);
+                if (!wait(&ld_v, ph ^ 1)) break;
+                start_y2();
+                give(&r_y2);
             } else if (last_part && a.S_T) {
 #pragma unroll 1
                 for (int x = 0; x < HP / 32; ++x) {
