@@ -19,8 +19,15 @@
 // G D,
 // dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
 //
-// Bound: 64 KB in and 16 KB out a unit at dk = 128 against 1500 cycles of
-// tensor pipe and about as many of the warps' arithmetic.
+// Bound: 64 KB in and 16 KB out a unit at dk = 128 (3500 cycles of an SM's share
+// of HBM) against 1500 cycles of tensor pipe.  Measured 9000 cycles a unit (8 x
+// 4096 tokens, 16 heads of 128: 330 us): X's elementwise part is the longest
+// stretch (3000), for its rows j <= i lie four blocks deep in the first
+// sub-partition of tensor memory and one deep in the last, and only a
+// sub-partition's own warps can read it.  Kept on measurement (same case): waits
+// of a dozen instructions and products issued by a converged warp 501 -> 436
+// us; the diagonal block without branches 393; no registers spilled 369; dq in
+// tensor memory, which frees 32 registers a thread, 331.
 #include "common.cuh"
 #include "ssm_tc.cuh"
 

@@ -2,28 +2,34 @@
 // tensor cores: the forward, the chain of states (or of their gradients) that
 // the backward reads, and the end states of a sequence's parts.
 //
-// A CTA of 16 warps takes one (sequence, head) -- or one part of it -- and
-// walks its chunks of 128 tokens with the fp32 state S [dk][dv] in tensor
-// memory.  In a chunk, with L_i the log decay from its start through token i,
+// A CTA takes one (sequence, head) -- or one part of it -- and walks its chunks
+// of 128 tokens with the fp32 state S [dk][dv] in tensor memory.  In a chunk,
+// with L_i the log decay from its start through token i,
 //     o_i = e^{L_i} S^T q_i + sum_{j <= i} M_ij v_j + skip v_i,
 //     M_ij = (q_i . k_j) e^{L_i - L_j} dt_j,
 //     S  <- e^{L_end} S + sum_j e^{L_end - L_j} dt_j k_j v_j^T,
-// as four products: G = q k^T; q S (S rounded to bf16); M v, with M = G masked,
-// decayed and rounded to bf16, written back to tensor memory as the left
-// operand; and the state's, whose left operand k e^{L_end - L_j} dt_j is taken
-// as two bf16 parts, so that S and S_T carry 16 bits of every factor.  The
-// chain of gradients E <- e^{L_end} E + sum_i e^{L_i} q_i do_i^T has the same
-// form, walked from the end.
+// as four products: G = q k^T; q S (S rounded to bf16); M v, with M formed from
+// G, rounded to bf16 and written over it in tensor memory as the left operand;
+// and the state's, whose left operand k e^{L_end - L_j} dt_j is taken as two
+// bf16 parts, so that S and S_T carry 16 bits of every factor (measured: S_T
+// 2e-6 from the exact state).  The chain of gradients
+// E <- e^{L_end} E + sum_i e^{L_i} q_i do_i^T has the same form, walked from the
+// end.
 //
-// Bounds: the forward reads q, k (shared by the group's heads, so mostly from
-// L2) and v and writes o once; its chunk costs 2560 cycles of tensor pipe at
-// dk = dv = 128 against 2800 of memory at full rate.  The products and the
-// read-backs of one chunk overlap (the state's product runs under M's
-// construction, M v under the state's read-back); tiles of the next chunk
-// arrive meanwhile: k two ahead, q as soon as this chunk's products have read
-// it, v at the chunk's end.  Every wait is bounded: where one runs out the
-// kernel records GDN2_ERR_TIMEOUT, lets its copies land, frees its tensor
-// memory and returns.
+// Bounds, at dk = dv = 128 and for a chunk: 64 KB of HBM traffic (v in, o out; q
+// and k come from L2, shared by the group's heads) take 2800 cycles of an SM's
+// share; the products take 2560 cycles of the tensor pipe, and read 256 KB of
+// operands from shared memory at its full 128 bytes a cycle; the warps and the
+// copies move another 350 KB through it.  So shared memory, at about 4800
+// cycles, bounds the chunk; measured 6700 (8 x 4096 tokens, 16 heads: 125 us
+// against 46 for the bytes at the rate of a plain copy).  What made the
+// difference on the way (same case): all warps in step 208 us; roles that meet
+// through mbarriers, without local memory 174; waits of a dozen instructions
+// and products issued by a converged warp (the code had outgrown the
+// instruction cache) 150; separate accumulators for q S and M v, o's tile over
+// q, the copies' waits off the issuer's path 125.  Every wait is bounded: where
+// one runs out the kernel records GDN2_ERR_TIMEOUT, lets its copies land, frees
+// its tensor memory and returns.
 #include "common.cuh"
 #include "ssm_tc.cuh"
 

@@ -346,7 +346,8 @@ int gdn2_output_gate_bwd(const void *o, const void *g, const float *gamma, const
  * Rows of q, k and v lie ldq, ldk and ldv elements apart (heads side by side
  * within a row), so that they may be views of one wider tensor, such as the
  * prologue's output; a fixed-length batch's sequences are T rows apart.  o, dO,
- * log_alpha and dt are contiguous.  q, k, v are 16-byte aligned, their row
+ * log_alpha (<= 0; any large negative value is a reset) and dt (>= 0) are
+ * contiguous; neither is checked.  q, k, v are 16-byte aligned, their row
  * strides a multiple of 16 bytes and at least their width; log_alpha and dt
  * need element alignment.  States are fp32 [B, H, dk, dv].  Sequences: B of T
  * tokens, or (cu_seqlens != null) a packed batch of B sequences in T rows, as
