@@ -18,6 +18,12 @@ namespace ssm {
 
 constexpr int kC = 64;  // tokens of a chunk of the fp32 kernels (the bf16 ones: 128)
 
+// A log decay as the chunks' sums take it: e^{-104} is 0 in fp32, so a stronger
+// decay changes nothing, and differences of the sums stay finite (-inf - -inf
+// would not).  A NaN stays one.
+constexpr float kLogMin = -104.f;
+__device__ __forceinline__ float bounded_log(float x) { return x < kLogMin ? kLogMin : x; }
+
 // Where sequence b's tokens lie; chunks of CH tokens.  Fixed length (cu ==
 // nullptr): rows b*T .. ; packed: rows cu[b] .. cu[b+1] - 1 of T rows in all.
 // `slot`: the per-chunk slot of its chunk 0.  A packed batch reserves slots

@@ -43,8 +43,8 @@ int check(int B, int T, int H, int G, int dk, int dv, int dtype) {
     if (dtype != GDN2_BF16 && dtype != GDN2_FP32) return GDN2_ERR_UNSUPPORTED;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return GDN2_ERR_UNSUPPORTED;
     if (H > 0 && (G < 1 || H % G != 0)) return GDN2_ERR_INVALID_ARG;
-    // grids and slot numbers stay within 31 bits
-    if ((long long)B * H > (1LL << 24) || (long long)B * T > 0x7fffffffLL) return GDN2_ERR_INVALID_ARG;
+    // grids, rows' widths and slot numbers stay within 31 bits
+    if (H > (1 << 16) || (long long)B * H > (1LL << 24) || (long long)B * T > 0x7fffffffLL) return GDN2_ERR_INVALID_ARG;
     return GDN2_OK;
 }
 // row strides: whole rows, and every row 16-byte aligned

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         g_la = g_dt = 0.f;
         if (i < nh && gt < len) {
             const size_t r = (grow + gt) * f.H + h_lo + i;
-            g_la = fmaxf(__bfloat162float(static_cast<const bf16 *>(f.la)[r]), kLogMin);
+            g_la = bounded_log(__bfloat162float(static_cast<const bf16 *>(f.la)[r]));
             g_dt = __bfloat162float(static_cast<const bf16 *>(f.dt)[r]);
         }
     };

@@ -665,7 +665,7 @@ bool f4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) 
 bool of4(const void *p) { return p == nullptr || f4(p); }
 
 int check(int B, int T, int C, int K, int H, int dtype, long long ldx, long long ldt) {
-    if (B < 0 || T < 0 || C < 0 || H < 0) return GDN2_ERR_INVALID_ARG;
+    if (B < 0 || T < 0 || C < 0 || H < 0 || (long long)B * T > 0x7fffffffLL) return GDN2_ERR_INVALID_ARG;
     if (dtype != GDN2_BF16 && dtype != GDN2_FP32) return GDN2_ERR_UNSUPPORTED;
     if (K < 1 || K > kMaxTaps || C % 8 != 0 || C > (1 << 20) || H > (1 << 16)) return GDN2_ERR_UNSUPPORTED;
     if (ldx < C || (H > 0 && ldt < H)) return GDN2_ERR_INVALID_ARG;

@@ -384,11 +384,11 @@ __global__ void __launch_bounds__(256, 1) chunk_bwd_kernel(ScanBwdArgs a) {
             // from the block's start through the token, lsu = from behind it to the
             // block's end, bs = the block's.  An exponent L_i - L_j across blocks
             // is then a sum of terms <= 0, which loses nothing where a chunk
-            // decays far.  A decay below e^{-104} is 0 in fp32, whatever its log.
+            // decays far.
             const int t = 2 * tid;
             const size_t r = (row + t) * f.H + h;
             const float *la = static_cast<const float *>(f.la), *dt = static_cast<const float *>(f.dt);
-            const float x0 = t < len ? fmaxf(la[r], -104.f) : 0.f, x1 = t + 1 < len ? fmaxf(la[r + f.H], -104.f) : 0.f;
+            const float x0 = t < len ? bounded_log(la[r]) : 0.f, x1 = t + 1 < len ? bounded_log(la[r + f.H]) : 0.f;
             float up = x0 + x1, dn = up;
 #pragma unroll
             for (int m = 1; m < 8; m <<= 1) {

@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, cons
             if (m >= kRing && !wait(&r_gfree[m % kRing], par(m - kRing, kRing))) break;
             const float all = form_gates_warp(gates[m % kRing], a.la, REV ? nullptr : a.dt, (size_t)sq.row0 * a.H + h, a.H,
                                               chunk_of(m) * kCT, sq.len, lane, carry);
-            if (LOCAL) carry = fmaxf(carry + all, 2.f * kLogMin);  // (as good as -inf; kept finite)
+            if (LOCAL) carry = carry + all < 2.f * kLogMin ? 2.f * kLogMin : carry + all;  // (as good as -inf; kept finite)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&r_gate[m % kRing]);
         }

@@ -19,7 +19,6 @@ namespace ssm {
 
 constexpr int kCT = 128;   // tokens of a chunk of the tensor-core kernels
 constexpr int kNT = 512;   // their threads: four warps per tensor-memory sub-partition
-constexpr float kLogMin = -104.f;  // e^{-104} is 0 in fp32: a stronger decay changes nothing
 
 // [B][T] rows, ld elements apart, of `heads` heads of D channels, in boxes of
 // 128 tokens x 64 channels of one head: coordinates (0, token, channel / 64, head, batch).
@@ -184,7 +183,7 @@ __device__ __forceinline__ float form_gates_warp(Gates &g, const void *la, const
     for (int e = 0; e < 4; ++e) {
         const int t = t0 + 4 * lane + e;
         const size_t r = first + (size_t)t * stride;
-        x[e] = t < len ? fmaxf(__bfloat162float(static_cast<const bf16 *>(la)[r]), kLogMin) : 0.f;
+        x[e] = t < len ? bounded_log(__bfloat162float(static_cast<const bf16 *>(la)[r])) : 0.f;
         d[e] = t >= len ? 0.f : dt ? __bfloat162float(static_cast<const bf16 *>(dt)[r]) : 1.f;
     }
     up[0] = x[0];

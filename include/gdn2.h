@@ -346,8 +346,11 @@ int gdn2_output_gate_bwd(const void *o, const void *g, const float *gamma, const
  * Rows of q, k and v lie ldq, ldk and ldv elements apart (heads side by side
  * within a row), so that they may be views of one wider tensor, such as the
  * prologue's output; a fixed-length batch's sequences are T rows apart.  o, dO,
- * log_alpha (<= 0; any large negative value is a reset) and dt (>= 0) are
- * contiguous; neither is checked.  q, k, v are 16-byte aligned, their row
+ * log_alpha (<= 0; a large negative value, -inf too, is a reset) and dt (>= 0)
+ * are contiguous; neither is checked.  An infinity or NaN elsewhere may reach
+ * every output of its own sequence, tokens before it included (they share a
+ * chunk's products), and no other's.  H <= 65536, B H <= 2^24 and B T < 2^31.
+ * q, k, v are 16-byte aligned, their row
  * strides a multiple of 16 bytes and at least their width; log_alpha and dt
  * need element alignment.  States are fp32 [B, H, dk, dv].  Sequences: B of T
  * tokens, or (cu_seqlens != null) a packed batch of B sequences in T rows, as

@@ -187,6 +187,35 @@ def test_resets_and_steps_of_zero(dtype):
 
 
 @pytest.mark.parametrize("dtype", SCAN)
+@pytest.mark.parametrize("T", [260, 2100])
+def test_resets_of_every_size_are_one(T, dtype):
+    """-inf and the type's lowest value, side by side too, give bit for bit
+    what -1e4 gives, in whole sequences, in parts and for a token; a NaN is
+    not mistaken for one."""
+    import gated_delta_rule_gdn2_b200 as g
+    d = dev(make(1, T, 2, 1, 64, 128, dtype, seed=14), dtype)
+    lowest = torch.finfo(TD[dtype]).min
+    at = [0, 3, 4, 5, 40, 63, 64, 127, 128, 200, 201, T - 1]
+
+    def run(*values):
+        la = d["la"].clone()
+        la[:, at] = torch.tensor([values[i % len(values)] for i in range(len(at))], dtype=la.dtype, device="cuda")[None, :, None]
+        a = [d["q"], d["k"], d["v"], la, d["dt"]]
+        o, ST, st = g.ssm_fwd(*a, skip=d["skip"], S0=d["S0"], save_states=True)
+        gr = g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], states=st)
+        S = d["S0"].clone()
+        o1 = g.ssm_step(*[t[:, 0].contiguous() for t in a], S, skip=d["skip"])
+        return [o, ST, o1, S] + [gr[n] for n in GRADS + ("dskip", "dS0")]
+
+    want = run(-1e4)
+    for s, t in zip(run(-float("inf"), lowest), want):
+        assert torch.equal(s, t)
+    o, ST = run(-1e4, float("nan"))[:2]
+    assert torch.isnan(o[:, 3:]).all() and torch.isnan(ST).all()
+    assert g.gdn2_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", SCAN)
 def test_neighbours_infinities_stay_out(dtype):
     """Packed: infinities and NaN in one sequence, and behind the last, reach
     no other; rows of no sequence are left as they were."""
@@ -580,3 +609,72 @@ def test_two_streams_at_once(dtype):
         for a, b in zip(got, want):
             for s, t in zip(a, b):
                 assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("dtype", SCAN)
+def test_stream_argument_and_rows_before_the_first_sequence(dtype):
+    """A stream by its handle while another is current, and offsets that start
+    behind row 0: the calls' results, and rows of no sequence as they were."""
+    import gated_delta_rule_gdn2_b200 as g
+    lens, ahead = (140, 0, 33), 9
+    x = make(3, ahead + sum(lens), 4, 2, 64, 64, dtype, lens=(ahead,) + lens, seed=71)
+    for n in ("S0", "dS_T"):
+        x[n] = x[n][:3]
+    d = dev(x, dtype)
+    rest = {n: d[n][ahead:].contiguous() for n in ("q", "k", "v", "la", "dt", "dO")}
+    cu0 = cu_of(lens)
+    cu1 = cu0 + ahead
+    names = ("q", "k", "v", "la", "dt")
+    W, bias, A, db = torch.randn(64, 4, device="cuda"), torch.randn(64, device="cuda"), torch.randn(4, device="cuda"), None
+
+    def run(y, cu, **kw):
+        a = [y[n] for n in names]
+        o, ST, st = g.ssm_fwd(*a, skip=d["skip"], S0=d["S0"], save_states=True, cu_seqlens=cu, **kw)
+        into = tuple(torch.full_like(t, 5.0) for t in a[:3])
+        kw.get("stream") and torch.cuda.current_stream().synchronize()
+        gr = g.ssm_bwd(*a, y["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], states=st, cu_seqlens=cu, into=into, **kw)
+        xx = y["v"].flatten(1)[:, :64]
+        pr = g.ssm_prologue(xx, W, bias, y["dt"], db, A, output_window=True, cu_seqlens=cu, **kw)
+        dx = xx.contiguous()
+        kw.get("stream") and torch.cuda.current_stream().synchronize()
+        gp = g.ssm_prologue_bwd(xx, W, bias, y["dt"], db, A, dx, y["dt"], y["la"], cu_seqlens=cu, **kw)
+        return ([o, pr[0], pr[1], pr[2], gp["dx"], gp["dxdt"]] + [gr[n] for n in GRADS],
+                [ST, pr[3], gp["dW"], gp["dbias"], gp["dA_log"], gr["dS0"]], into)
+
+    rows, whole, _ = run(rest, cu0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for kw in ({}, {"stream": side}, {"stream": side.cuda_stream}):
+        r1, w1, into = run(d, cu1, **kw)
+        side.synchronize()
+        for s, t in zip(rows[:6], r1[:6]):
+            assert torch.equal(s, t[ahead:])
+        for s, t in zip(whole[:2], w1[:2]):
+            assert torch.equal(s, t)
+        # (the sums over every token meet other rows in a block, and the packed slots move: fp32 sums in another order)
+        for s, t in zip(whole[2:5], w1[2:5]):
+            assert (s - t).norm() <= 1e-5 * s.norm()
+        for s, t in zip(rows[6:], r1[6:]):
+            assert torch.equal(s, t[ahead:])
+        assert torch.equal(whole[5], w1[5])
+        for t in into:
+            assert torch.all(t[:ahead] == 5.0)
+    assert g.gdn2_get_device_status() == 0
+
+
+def test_batches_and_sequences_of_nothing():
+    import gated_delta_rule_gdn2_b200 as g
+    for B, T in ((0, 5), (2, 0)):
+        e = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+        q, v, la, S0 = e(B, T, 1, 64), e(B, T, 2, 64), e(B, T, 2), torch.randn(B, 2, 64, 64, device="cuda")
+        o, ST, st = g.ssm_fwd(q, q, v, -la, la, skip=e(2), S0=S0, save_states=True)
+        gr = g.ssm_bwd(q, q, v, -la, la, v, skip=e(2), S0=S0, dS_T=2 * S0, states=st)
+        assert o.shape == v.shape and torch.equal(ST, S0) and torch.equal(gr["dS0"], 2 * S0)
+        assert gr["dq"].shape == q.shape and torch.all(gr["dskip"] == 0)
+        x, W, init = e(B, T, 8), e(8, 4), torch.randn(B, 3, 8, device="cuda")
+        y, dt, a, win = g.ssm_prologue(x, W, e(8), la, e(2), e(2), init=init, output_window=True)
+        assert y.shape == x.shape and torch.equal(win, init) and dt.shape == la.shape
+        gp = g.ssm_prologue_bwd(x, W, e(8), la, e(2), e(2), x, la, la, init=init)
+        assert torch.all(gp["dW"] == 0) and torch.all(gp["dA_log"] == 0) and torch.all(gp["dinit"] == 0)
+    assert g.ssm_step(e(0, 1, 64), e(0, 1, 64), e(0, 2, 64), e(0, 2), e(0, 2), e(0, 2, 64, 64)).shape == (0, 2, 64)
+    assert g.gdn2_get_device_status() == 0

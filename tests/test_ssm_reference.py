@@ -122,6 +122,7 @@ def _fwd(**kw):
     (dict(o=None), -1), (dict(la=None), -1), (dict(la=17), -1), (dict(dt=17), -1), (dict(S0=8), -1), (dict(skip=18), -1),
     (dict(ldq=64), -1), (dict(ldk=132), -1), (dict(ldv=255), -1), (dict(ldv=260), -1), (dict(cu=18), -1),
     (dict(states=40), -1), (dict(B=1 << 20, H=64, ldv=8192), -1),
+    (dict(H=1 << 24, ldv=1 << 31), -1), (dict(B=1 << 20, T=1 << 11), -1),
 ])
 def test_scan_refuses(kw, code):
     assert _fwd(**kw) == code
@@ -179,6 +180,7 @@ PRO = dict(x=P, W=P, bias=None, K=4, xdt=P, dt_bias=None, A_log=P, init=None, y=
     (dict(ldt=1), -1), (dict(x=None), -1), (dict(x=17), -1), (dict(W=None), -1), (dict(W=6), -1), (dict(y=24), -1),
     (dict(init=8), -1), (dict(window=8), -1), (dict(xdt=None), -1), (dict(A_log=None), -1), (dict(dt=None), -1),
     (dict(cu=18), -1), (dict(bias=2), -1), (dict(B=0), 0), (dict(T=0), 0), (dict(C=0, H=0), 0),
+    (dict(B=1 << 20, T=1 << 11), -1),
 ])
 def test_prologue_refuses(kw, code):
     assert g.gdn2_ssm_prologue_fwd(*{**PRO, **kw}.values(), 0) == code
