@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                        idZq = tc::idesc_bf16(128, N, true, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t ld_qk, ld[2], b_x, b_y, b_c, b_d, b_e, b_z;
+    __shared__ uint64_t ld_qk, ldx[2], ld[2], b_x, b_y, b_c, b_d, b_z;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
 
     if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        uint64_t *bars[] = {&ld_qk, &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_e, &b_z};
+        uint64_t *bars[] = {&ld_qk, &ldx[0], &ldx[1], &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_z};
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
         tc::fence_mbar_init();
         dead = 0;
@@ -154,9 +154,10 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         if (!elect()) return;
         const int s = u & 1, h = h_lo + u / NX, x = u % NX;
         unsigned char *st = sm + L::ST0 + s * L::STAGE;
-        tc::mbar_expect_tx(&ld[s], L::STAGE);
-        tc::tma_load_5d(st, &maps.v, 0, mt, x, h, mb, &ld[s]);
-        tc::tma_load_5d(st + L::VB, &maps.dO, 0, mt, x, h, mb, &ld[s]);
+        tc::mbar_expect_tx(&ldx[s], 2 * L::VB);
+        tc::tma_load_5d(st, &maps.v, 0, mt, x, h, mb, &ldx[s]);
+        tc::tma_load_5d(st + L::VB, &maps.dO, 0, mt, x, h, mb, &ldx[s]);
+        tc::mbar_expect_tx(&ld[s], 2 * L::SB);
         const size_t img = ((size_t)slot * f.H + h) * (N * P * 2) + (size_t)x * L::SB;
         tc::bulk_load(st + 2 * L::VB, static_cast<const unsigned char *>(a.grads) + img, L::SB, &ld[s]);
         tc::bulk_load(st + 2 * L::VB + L::SB, static_cast<const unsigned char *>(f.states) + img, L::SB, &ld[s]);
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         form_bwd_gates(gates[0], g_la, g_dt, gt);
         load_gates(1);
     }
-    for (int i = tid; i < 17 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp, colp, rp, up, cd lie side by side)
+    for (int i = tid; i < 8 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp and colp: those of masked blocks stay zero)
 
     // ---- G^T = k q^T, kept as bf16 pairs in tensor memory
     wait(&ld_qk, 0);
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     }
     handoff();
 
-    float Z[32], es = 0.f, dsk = 0.f, q_dq = 0.f;  // q_dq: q . dq so far
+    float Z[32], es = 0.f, dsk = 0.f, rs = 0.f, q_dq = 0.f;  // rs: r of token j = row; q_dq: q . dq up to the head before
 #pragma unroll
     for (int i = 0; i < 32; ++i) Z[i] = 0.f;
 
@@ -259,15 +260,15 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 static_cast<bf16 *>(a.ddt)[at + (size_t)e * f.H] = __float2bfloat16_rn(dd[e]);
             }
     };
-    // X of unit u (its stage has landed)
+    // X of a head, summed over its units (whose v and dO have landed)
     auto product_X = [&](int u) {
         if (!elect()) return;
         const unsigned char *v = sm + L::ST0 + (u & 1) * L::STAGE;
-        mma_tiles<true, true>(tm + cX, v, kCT, v + L::VB, kCT, 4, idX, false);
-        tc::commit(&b_x);
+        mma_tiles<true, true>(tm + cX, v, kCT, v + L::VB, kCT, 4, idX, u % NX > 0);
+        if (u % NX == NX - 1) tc::commit(&b_x);
     };
     if (warp == kIssuer && nu > 0 && !tail) {
-        wait(&ld[0], 0);
+        wait(&ldx[0], 0);
         product_X(0);
     }
     for (int u = 0; u < nu && !aborted; ++u) {
@@ -275,22 +276,30 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         const uint32_t ph = u & 1, ph2 = (u >> 1) & 1;
         const BwdGates &G = gates[hh & 1];
         unsigned char *sV = sm + L::ST0 + s * L::STAGE, *sO = sV + L::VB, *sE = sO + L::VB, *sS = sE + L::SB;
-        wait(&ld[s], ph2);
-        if (tail) {
-            zero_tail(sV, 1, len, tid, kNT);
-            zero_tail(sO, 1, len, tid, kNT);
+        wait(&ldx[s], ph2);
+        if (tail && x == 0) {
+            if (NX > 1) wait(&ldx[1], ph2);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                unsigned char *v = sm + L::ST0 + ((s + i) & 1) * L::STAGE;
+                zero_tail(v, 1, len, tid, kNT);
+                zero_tail(v + L::VB, 1, len, tid, kNT);
+            }
             handoff();
             if (aborted) break;
+            if (warp == kIssuer)
+#pragma unroll
+                for (int i = 0; i < NX; ++i) product_X(u + i);
         }
+        wait(&ld[s], ph2);
         if (warp == kIssuer) {
-            if (tail) product_X(u);
             if (elect()) {
                 mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
                 tc::commit(&b_y);
             }
-            if (u > 0 && u + 1 < nu) {  // the other stage: free once its last product is done
-                wait(&b_e, (u - 1) & 1);
-                load(u + 1);
+            if (!tail && NX > 1 && x == 0) {  // the rest of X
+                wait(&ldx[1], ph2);
+                product_X(u + 1);
             }
         }
         const float dtj = G.dt[row];
@@ -312,10 +321,41 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             asm volatile("bar.sync 2, 512;\n" ::: "memory");
             if (warp == kFinisher) finish(hh - 1);  // (this warp has no part in X below)
         }
-        wait(&b_x, ph);
+        // ---- Y: token j = row, value columns 16 qc ..
+        wait(&b_y, ph);
         tc::fence_after();
-        // ---- X: token j = row, tokens i = 32 qc ..; (G D)^T over the columns read
-        if (qc < p) {
+        {
+            float y[16];
+            ld16(tl + cY + 16 * qc, y);
+            const float w = G.wt[row], wd = w * dtj;
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = piece(kCT, row, 2 * qc + i);
+                const uint4 v = *reinterpret_cast<const uint4 *>(sV + at), o = *reinterpret_cast<const uint4 *>(sO + at);
+                uint32_t ve[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 vv = unpack2(ve[e]), oo = unpack2(oe[e]);
+                    const int c = 8 * i + 2 * e;
+                    dsk = fmaf(vv.x, oo.x, fmaf(vv.y, oo.y, dsk));
+                    y[c] *= w;
+                    y[c + 1] *= w;
+                    rs = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, rs));
+                    ve[e] = pack2(vv.x * wd, vv.y * wd);
+                }
+                *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
+            }
+            stw<16>(tl + cY + 16 * qc, y);
+        }
+        // ---- X of the head: token j = row, tokens i = 32 qc ..; (G D)^T over the columns read
+        if (x == 0) {
+            wait(&b_x, hh & 1);
+            tc::fence_after();
+        }
+        if (x > 0) {
+        } else if (qc < p) {
             const uint32_t z[16] = {0};
             st16(tl + cX + 32 * qc, z);
         } else {
@@ -373,44 +413,26 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                     X[i] = t.x;
                     X[i + 1] = t.y;
                 }
-                const float rs = lane_sums16(X, lane);
-                if ((lane & 1) == 0) rowp[p][32 * qc + c0 + (lane >> 1)] += rs;
+                const float sum = lane_sums16(X, lane);
+                if ((lane & 1) == 0) rowp[p][32 * qc + c0 + (lane >> 1)] = sum;
             }
-            colp[qc][row] += col2.x + col2.y;
-            if (dg) cd[row] += diag;
+            colp[qc][row] = col2.x + col2.y;
+            if (dg) cd[row] = diag;
         }
-        // ---- Y: token j = row, value columns 16 qc ..
-        wait(&b_y, ph);
-        tc::fence_after();
-        {
-            float y[16];
-            ld16(tl + cY + 16 * qc, y);
-            const float w = G.wt[row], wd = w * dtj, er = G.er[row];
-            uint32_t eo[8];  // e^{L_i} dO_i, for dq: beside (G D)^T, over columns of X that this thread has read
-            tc::wait_ld();
-            float r = 0.f;
+        {  // e^{L_i} dO_i, for dq: beside (G D)^T, over columns of X that this warp has read
+            const float er = G.er[row];
+            uint32_t eo[8];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t at = piece(kCT, row, 2 * qc + i);
-                const uint4 v = *reinterpret_cast<const uint4 *>(sV + at), o = *reinterpret_cast<const uint4 *>(sO + at);
-                uint32_t ve[4] = {v.x, v.y, v.z, v.w};
+                const uint4 o = *reinterpret_cast<const uint4 *>(sO + piece(kCT, row, 2 * qc + i));
                 const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 vv = unpack2(ve[e]), oo = unpack2(oe[e]);
-                    const int c = 8 * i + 2 * e;
-                    dsk = fmaf(vv.x, oo.x, fmaf(vv.y, oo.y, dsk));
-                    y[c] *= w;
-                    y[c + 1] *= w;
-                    r = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, r));
-                    ve[e] = pack2(vv.x * wd, vv.y * wd);
+                    const float2 oo = unpack2(oe[e]);
                     eo[4 * i + e] = pack2(oo.x * er, oo.y * er);
                 }
-                *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
             }
-            stw<16>(tl + cY + 16 * qc, y);
             st8(tl + cX + 32 * qc + 16, eo);
-            rp[qc][row] += r;
             tc::wait_st();
         }
         if (x == NX - 1) {
@@ -419,7 +441,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 red[warp] = e2;
                 red[16 + warp] = d2;
             }
-            es = dsk = 0.f;
+            rp[qc][row] = rs;
+            es = dsk = rs = 0.f;
         }
         if (x == 0 && gt >= 0) {
             form_bwd_gates(gates[(hh + 1) & 1], g_la, g_dt, gt);
@@ -434,13 +457,12 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             for (int i = 0; i < kCT / 16; ++i)
                 mma_ts(tm + cY, tm + cX + 32 * (i >> 1) + 8 * (i & 1), o0 + (tct::kstep_bytes<false>(kCT, i) >> 4), idY, true);
             tc::commit(&b_c);
+            mma_tiles<true, true>(tm + cDK, sV, kCT, sE, N, 4, idN, u > 0);
             const uint64_t s0 = tct::kmaj(sS, N, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 mma_ts(tm + cDQ, tm + cX + 32 * i + 16, s0 + (tct::kstep_bytes<true>(N, i) >> 4), idN, u > 0 || i > 0);
             tc::commit(&b_d);
-            mma_tiles<true, true>(tm + cDK, sV, kCT, sE, N, 4, idN, u > 0);
-            tc::commit(&b_e);
         }
         wait(&b_c, ph);
         tc::fence_after();
@@ -463,9 +485,9 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 *reinterpret_cast<uint4 *>(sm + L::STG + at) = make_uint4(oe[0], oe[1], oe[2], oe[3]);
             }
         }
-        wait(&b_d, ph);
-        tc::fence_after();
-        {  // u_i = q_i . (what this unit added to dq_i): key channels WN qc ..
+        if (x == NX - 1) {  // u_i = q_i . (what the head added to dq_i): key channels WN qc ..
+            wait(&b_d, ph);
+            tc::fence_after();
             float us = 0.f;
 #pragma unroll
             for (int hf = 0; hf < WN / 16; ++hf) {
@@ -483,15 +505,19 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                     us = fmaf(qq.x, t[2 * e], fmaf(qq.y, t[2 * e + 1], us));
                 }
             }
-            up[qc][row] += us - q_dq;
+            up[qc][row] = us - q_dq;
             q_dq = us;
         }
-        if (warp == kIssuer && !tail && u + 1 < nu) {  // the next X (the products that read (G D)^T and e^L dO are done)
-            wait(&ld[s ^ 1], (uint32_t)((u + 1) >> 1) & 1u);
-            product_X(u + 1);
+        if (warp == kIssuer) {
+            wait(&b_d, ph);
+            if (!tail && x == NX - 1 && u + 1 < nu) {  // the next X (the products that read (G D)^T and e^L dO are done)
+                wait(&ldx[s ^ 1], (uint32_t)((u + 1) >> 1) & 1u);
+                product_X(u + 1);
+            }
         }
         handoff();
         if (aborted) break;
+        if (warp == kIssuer && u + 2 < nu) load(u + 2);  // (the stage's products and reads are done)
         if (warp == kIssuer && !tail && elect()) {
             tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
             tc::bulk_commit();
@@ -502,18 +528,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 *reinterpret_cast<uint4 *>(dv + (size_t)(i / 8) * f.ldv + 8 * (i % 8)) =
                     *reinterpret_cast<const uint4 *>(sm + L::STG + piece(kCT, i / 8, i % 8));
         }
-        if (x == NX - 1 && p == 3) {  // the head's sums of token 32 qc + lane, left at zero for the next head
+        if (x == NX - 1 && p == 3) {  // the head's sums of token 32 qc + lane
             const int t = 32 * qc + lane;
-            auto take = [&](float(*part)[kCT]) {
-                const float v = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
-                part[0][t] = part[1][t] = part[2][t] = part[3][t] = 0.f;
-                return v;
-            };
+            auto take = [&](const float(*part)[kCT]) { return (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]); };
             const float ro = take(rowp), co = take(colp), r = take(rp), uu = take(up), dt = G.dt[t];
             fin[t] = uu + ro - dt * co;
             fin[kCT + t] = dt * r;
             fin[2 * kCT + t] = r + co + cd[t];
-            cd[t] = 0.f;
             if (warp == kFinisher) {
                 eall = warp_sum(lane < 16 ? red[lane] : 0.f) * G.gamma;
                 dall = warp_sum(lane < 16 ? red[16 + lane] : 0.f);
@@ -524,7 +545,6 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     if (!aborted && nu > 0 && warp == kFinisher) finish(nh - 1);
 
     // ---- dq += Z k, dk += Z^T q, and out
-    if (!aborted && nu > 0) wait(&b_e, (nu - 1) & 1);
     if (!aborted) {
         put_row<32>(sm + L::ST0, kCT, row, 32 * qc, Z);
     }
@@ -566,8 +586,10 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             tc::bulk_wait();
         }
         if (aborted) (void)tc::mbar_wait(&b_z, 1);
-        if (nl > 0) (void)tc::mbar_wait(&ld[0], ((nl - 1) >> 1) & 1);
-        if (nl > 1) (void)tc::mbar_wait(&ld[1], ((nl - 2) >> 1) & 1);
+        for (int i = 0; i < 2 && i < nl; ++i) {
+            (void)tc::mbar_wait(&ldx[i], ((nl - 1 - i) >> 1) & 1);
+            (void)tc::mbar_wait(&ld[i], ((nl - 1 - i) >> 1) & 1);
+        }
     }
     tc::fence_before();
     __syncthreads();
