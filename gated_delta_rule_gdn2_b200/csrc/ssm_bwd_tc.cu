@@ -38,7 +38,7 @@ namespace {
 using tct::mma_tiles;
 
 // Warps 3 and 7 (last sub-partition, first token blocks) have no part in X:
-// one issues the copies and products, the other writes a head's dla and ddt.
+// one issues the products, the other the copies, and writes a head's dla and ddt.
 constexpr int kIssuer = 3, kFinisher = 7;
 
 struct BwdMaps {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         aborted = __syncthreads_or(bad);
         tc::fence_after();
     };
-    if (warp == kIssuer) {
+    if (warp == kFinisher) {
         if (elect()) {
             tc::mbar_expect_tx(&ld_qk, 2 * L::QB);
             for (int x = 0; x < N / 64; ++x) {
@@ -186,19 +186,19 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     }
     // the warps of the last sub-partition, which have the least of X, form the
     // decay factors, one head ahead
-    float g_la = 0.f, g_dt = 0.f;
+    bf16 g_la, g_dt;  // as loaded: nothing waits for them before they are used
     const int gt = p == 3 ? 32 * qc + lane : -1;
     auto load_gates = [&](int i) {
-        g_la = g_dt = 0.f;
+        g_la = g_dt = __ushort_as_bfloat16(0);
         if (i < nh && gt < len) {
             const size_t r = (grow + gt) * f.H + h_lo + i;
-            g_la = bounded_log(__bfloat162float(static_cast<const bf16 *>(f.la)[r]));
-            g_dt = __bfloat162float(static_cast<const bf16 *>(f.dt)[r]);
+            g_la = static_cast<const bf16 *>(f.la)[r];
+            g_dt = static_cast<const bf16 *>(f.dt)[r];
         }
     };
     if (gt >= 0) {
         load_gates(0);
-        form_bwd_gates(gates[0], g_la, g_dt, gt);
+        form_bwd_gates(gates[0], bounded_log(__bfloat162float(g_la)), __bfloat162float(g_dt), gt);
         load_gates(1);
     }
     for (int i = tid; i < 8 * kCT; i += kNT) (&rowp[0][0])[i] = 0.f;  // (rowp and colp: those of masked blocks stay zero)
@@ -267,9 +267,18 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         mma_tiles<true, true>(tm + cX, v, kCT, v + L::VB, kCT, 4, idX, u % NX > 0);
         if (u % NX == NX - 1) tc::commit(&b_x);
     };
-    if (warp == kIssuer && nu > 0 && !tail) {
-        wait(&ldx[0], 0);
-        product_X(0);
+    auto product_Y = [&](int u) {
+        wait(&ld[u & 1], (uint32_t)(u >> 1) & 1u);
+        if (!elect()) return;
+        mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sm + L::ST0 + (u & 1) * L::STAGE + 2 * L::VB, N, N / 16, idY, false);
+        tc::commit(&b_y);
+    };
+    if (warp == kIssuer && nu > 0) {
+        if (!tail) {
+            wait(&ldx[0], 0);
+            product_X(0);
+        }
+        product_Y(0);
     }
     for (int u = 0; u < nu && !aborted; ++u) {
         const int s = u & 1, hh = u / NX, x = u % NX, h = h_lo + hh;
@@ -292,16 +301,6 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 for (int i = 0; i < NX; ++i) product_X(u + i);
         }
         wait(&ld[s], ph2);
-        if (warp == kIssuer) {
-            if (elect()) {
-                mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sE, N, N / 16, idY, false);
-                tc::commit(&b_y);
-            }
-            if (!tail && NX > 1 && x == 0) {  // the rest of X
-                wait(&ldx[1], ph2);
-                product_X(u + 1);
-            }
-        }
         const float dtj = G.dt[row];
         // <E, S> (the two images have one layout), by the warps with the least of X
         if (p >= 2) {
@@ -317,9 +316,14 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 }
             }
         }
-        if (u > 0 && x == 0) {  // the head before is summed up
-            asm volatile("bar.sync 2, 512;\n" ::: "memory");
+        if (x == 0 && u > 0) {  // the head before is summed up; its parts may be overwritten
+            if (NX == 1) asm volatile("bar.sync 2, 512;\n" ::: "memory");
+            else if (p == 3) asm volatile("bar.sync 1, 128;\n" ::: "memory");  // (the other warps wait for X, which comes after)
             if (warp == kFinisher) finish(hh - 1);  // (this warp has no part in X below)
+        }
+        if (!tail && NX > 1 && x == 0 && warp == kIssuer) {  // the rest of X
+            wait(&ldx[1], ph2);
+            product_X(u + 1);
         }
         // ---- Y: token j = row, value columns 16 qc ..
         wait(&b_y, ph);
@@ -445,10 +449,10 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             es = dsk = rs = 0.f;
         }
         if (x == 0 && gt >= 0) {
-            form_bwd_gates(gates[(hh + 1) & 1], g_la, g_dt, gt);
+            form_bwd_gates(gates[(hh + 1) & 1], bounded_log(__bfloat162float(g_la)), __bfloat162float(g_dt), gt);
             load_gates(hh + 2);
         }
-        if (warp == kIssuer && elect()) tc::bulk_wait_read();  // the dv tile of the unit before
+        if (warp == kFinisher && elect()) tc::bulk_wait_read();  // the dv tile of the unit before
         handoff();
         if (aborted) break;
         if (warp == kIssuer && elect()) {
@@ -517,10 +521,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         handoff();
         if (aborted) break;
-        if (warp == kIssuer && u + 2 < nu) load(u + 2);  // (the stage's products and reads are done)
-        if (warp == kIssuer && !tail && elect()) {
-            tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
-            tc::bulk_commit();
+        if (warp == kIssuer && u + 1 < nu) product_Y(u + 1);
+        if (warp == kFinisher) {
+            if (u + 2 < nu) load(u + 2);  // (the stage's products and reads are done)
+            if (!tail && elect()) {
+                tma_store_5d(&maps.dv, sm + L::STG, mt, x, h, mb);
+                tc::bulk_commit();
+            }
         }
         if (tail) {
             bf16 *dv = static_cast<bf16 *>(a.dv) + grow * f.ldv + (size_t)h * P + 64 * x;
@@ -580,12 +587,12 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             }
         }
     }
-    if (warp == kIssuer) {  // nothing is left in flight
-        if (elect()) {
-            if (aborted) tc::commit(&b_z);
-            tc::bulk_wait();
-        }
-        if (aborted) (void)tc::mbar_wait(&b_z, 1);
+    if (aborted && warp == kIssuer) {  // nothing is left in flight
+        if (elect()) tc::commit(&b_z);
+        (void)tc::mbar_wait(&b_z, 1);
+    }
+    if (warp == kFinisher) {
+        if (elect()) tc::bulk_wait();
         for (int i = 0; i < 2 && i < nl; ++i) {
             (void)tc::mbar_wait(&ldx[i], ((nl - 1 - i) >> 1) & 1);
             (void)tc::mbar_wait(&ld[i], ((nl - 1 - i) >> 1) & 1);
