@@ -95,6 +95,7 @@ struct ScanArgs {
     // part_state / part_decay: [B][H][parts - 1] end states (from zero) and decays
     int parts;
     float *part_state, *part_decay;
+    bool sorted;        // (bf16) blocks take the sequences by length, longest first
 };
 
 struct ScanBwdArgs {
