@@ -1,13 +1,16 @@
 """One workload of the benchmark, run on its own for an ncu capture.
 
-    python -m gated_delta_rule_gdn2_b200.profile_case {train,prefill,decode,long} [--batch B] [--T T] [--reps N]
+    python -m gated_delta_rule_gdn2_b200.profile_case {train,prefill,decode,long,ssm} [--batch B] [--T T] [--reps N]
 
 train: gdn2_chunk_fwd_save then gdn2_chunk_bwd_saved (B x T4096 x H16, d 128),
 N times each; prefill: gdn2_chunk_fwd at that shape; decode: gdn2_decode_step
 at B256 H16 (fp32 state in place); long: gdn2_chunk_fwd at B1 H16 and the given
-T.  Inputs are drawn on the device from the benchmark's distributions, so a
+T; ssm: a state space layer's prologue, scan (states kept), the scan's backward
+and the prologue's at the same shape, q and k shared by all heads.  Inputs are drawn on the device from the benchmark's distributions, so a
 capture starts within seconds.  Launch order per rep: train = forward, then
-backward; the others one kernel (the segmented long forward: its passes).
+backward; ssm = prologue, scan, chain of state gradients, scan backward, a sum,
+prologue backward, a sum; the others one kernel (the segmented long forward: its
+passes).
 """
 from __future__ import annotations
 
@@ -20,7 +23,7 @@ def main():
     from gated_delta_rule_gdn2_b200.inputs import make_inputs_device
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["train", "prefill", "decode", "long"])
+    ap.add_argument("case", choices=["train", "prefill", "decode", "long", "ssm"])
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--T", type=int, default=4096)
     ap.add_argument("--reps", type=int, default=2)
@@ -29,7 +32,20 @@ def main():
     D, H = 128, 16
     sh = torch.cuda.current_stream().cuda_stream
     names = ("q", "k", "v", "log_alpha", "b", "w")
-    if a.case == "decode":
+    if a.case == "ssm":
+        B, T, C = a.batch, a.T, H * D + 2 * D
+        r = lambda *s: torch.randn(s, device=dev).to(torch.bfloat16)  # noqa: E731
+        x, xdt, dO = r(B, T, C), r(B, T, H) - 3, r(B, T, H, D)
+        W, bias, A_log, skip = torch.randn(C, 4, device=dev) / 2, torch.zeros(C, device=dev), torch.zeros(H, device=dev), torch.ones(H, device=dev)
+        dy = torch.empty_like(x)
+        cut = lambda y: (y[..., H * D + D:].unflatten(-1, (1, D)), y[..., H * D:H * D + D].unflatten(-1, (1, D)),  # noqa: E731
+                         y[..., :H * D].unflatten(-1, (H, D)))
+        for _ in range(a.reps):
+            y, dt, la, _ = g.ssm_prologue(x, W, bias, xdt, None, A_log)
+            _, _, states = g.ssm_fwd(*cut(y), la, dt, skip=skip, save_states=True)
+            gr = g.ssm_bwd(*cut(y), la, dt, dO, skip=skip, states=states, need_dS0=False, into=cut(dy))
+            g.ssm_prologue_bwd(x, W, bias, xdt, None, A_log, dy, gr["ddt"], gr["dlog_alpha"])
+    elif a.case == "decode":
         B = 256
         x = make_inputs_device(B, 1, H, D, D, seed=1002, device=dev)
         toks = [x[n][:, 0].contiguous() for n in names]
