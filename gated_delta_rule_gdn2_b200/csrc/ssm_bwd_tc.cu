@@ -5,29 +5,31 @@
 // and goes through the heads, 64 value columns at a time ("a unit": v, dO and
 // the matching columns of the state S at the chunk's start and of the gradient
 // E at its end, 64 KB, double buffered).  With the factors of ssm_scan.cu,
-// G = q k^T kept once per CTA and D_ij the decay from j to i, a unit is
+// G = q k^T kept once per CTA and D_ij the decay from j to i, a head is
 //     X = v dO^T            -> W = G D X: sums for dla and ddt; Z += D X dt
-//     Y = k E               -> r_j = w_j Y_j . v_j; Y scaled by w_j
+// over both of its units, and a unit
+//     Y = k E               -> r_j += w_j Y_j . v_j; Y scaled by w_j
 //     Y += (G D)^T dO       -> dv = dt Y + skip dO
-//     dq += (e^L dO) S^T    -> u_i = q_i . (what it added)
+//     dq += (e^L dO) S^T    -> u_i = q_i . (what the head added)
 //     dk += (dt w v) E^T
 // and behind the last head dq += Z k, dk += Z^T q, so that both are summed over
 // the heads before they are rounded.  Rows of X, Y are tokens j (lanes of
 // tensor memory), columns i, so that (G D)^T is written back to tensor memory
 // as the left operand of the third product; the sums over j of W's columns are
-// a transposing reduction within each warp.  Operands rounded to bf16: G,
-// G D,
-// dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
+// a transposing reduction within each warp.  Operands rounded to bf16: G, G D,
+// e^L dO, dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
 //
 // Bound: 64 KB in and 16 KB out a unit at dk = 128 (3500 cycles of an SM's share
-// of HBM) against 1500 cycles of tensor pipe.  Measured 9000 cycles a unit (8 x
-// 4096 tokens, 16 heads of 128: 330 us): X's elementwise part is the longest
-// stretch (3000), for its rows j <= i lie four blocks deep in the first
-// sub-partition of tensor memory and one deep in the last, and only a
-// sub-partition's own warps can read it.  Kept on measurement (same case): waits
-// of a dozen instructions and products issued by a converged warp 501 -> 436
-// us; the diagonal block without branches 393; no registers spilled 369; dq in
-// tensor memory, which frees 32 registers a thread, 331.
+// of HBM) against 1500 cycles of tensor pipe.  Measured 8300 cycles a unit (8 x
+// 4096 tokens, 16 heads of 128: 281 us; 256 blocks, so a wave and three
+// quarters), 48% of the issue slots: X's elementwise part is the longest
+// stretch, for its rows j <= i lie four blocks deep in the first sub-partition
+// of tensor memory and one deep in the last, and only a sub-partition's own
+// warps can read it.  Kept on measurement (same case): waits of a dozen
+// instructions and products issued by a converged warp 501 -> 436 us; the
+// diagonal block without branches 393; no registers spilled 369; dq in tensor
+// memory, which frees 32 registers a thread, 331; X and u once a head 295; no
+// warp waits for the next head's decays as they are loaded 281.
 #include "common.cuh"
 #include "ssm_tc.cuh"
 
