@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             wait(&ldx[1], ph2);
             product_X(u + 1);
         }
-        // ---- Y: token j = row, value columns 16 qc ..
+        // ---- Y: token j = row, value columns 16 qc ..  (v is overwritten: X has read this unit's before Y, or, behind a
+        // sequence's end, where it was issued after, is waited for)
+        if (tail && x == 0) wait(&b_x, hh & 1);
         wait(&b_y, ph);
         tc::fence_after();
         {
