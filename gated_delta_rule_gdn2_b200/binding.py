@@ -710,14 +710,17 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _row_ld(name, t, lead, width):
-    """Elements between the rows of t [*lead, *inner], whose inner dimensions
-    are contiguous and whose leading ones are rows at one distance."""
-    if t.shape[:len(lead)] != lead:
-        raise ValueError("%s must have leading dimensions %s, got %s" % (name, tuple(lead), tuple(t.shape)))
+def _row_ld(name, t, n, width):
+    """Elements between the rows of t, whose inner dimensions are contiguous
+    and whose n leading ones are rows at one distance."""
     if t.is_contiguous():
         return width
-    n, st, sh = len(lead), t.stride(), t.shape
+    st, sh = t.stride(), t.shape
+    if st[-1] == 1 and (len(st) == n + 1 or st[-2] == sh[-1]):  # slices of wider rows, in few steps
+        if n == 1 and sh[0] > 1:
+            return st[0]
+        if n == 2 and sh[1] > 1 and (sh[0] == 1 or st[0] == st[1] * sh[1]):
+            return st[1]
     step = 1
     for d in range(t.dim() - 1, n - 1, -1):
         if sh[d] != 1 and st[d] != step:
@@ -734,47 +737,58 @@ def _row_ld(name, t, lead, width):
     return width if ld is None else ld
 
 
-def _check_like(name, t, shape, ref):
-    """A contiguous tensor of ref's dtype and device."""
-    if t.shape != shape or t.dtype != ref.dtype or t.get_device() != ref.get_device() or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, ref.dtype, tuple(shape), ref.device))
+def _check_like(name, t, shape, dtype, dev):
+    """A contiguous tensor of this shape and dtype on device number dev."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (name, dtype, tuple(shape), dev))
 
 
-def _check_f32(name, t, shape, ref):
+def _check_f32(name, t, shape, dev):
     import torch
-    if t is not None and (t.shape != shape or t.dtype != torch.float32 or t.get_device() != ref.get_device() or
-                          not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous fp32 tensor of shape %s on %s" % (name, tuple(shape), ref.device))
+    _check_like(name, t, shape, torch.float32, dev)
+
+
+def _empty_as(t):
+    """An empty contiguous tensor of t's shape, dtype and device (empty_like
+    takes half the time of new_empty with a shape)."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, lead_dims):
     if cu_seqlens is not None:
         lead_dims = 1
-    vs, qs = v.shape, q.shape
+    vs, qs, dtype, dev = v.shape, q.shape, q.dtype, q.get_device()
     if len(vs) != lead_dims + 2 or len(qs) != lead_dims + 2:
         raise ValueError("v must be %s + (H, dv) and q, k (G, dk)" % ("[rows]" if lead_dims == 1 else "[B, T]"))
-    lead, (H, dv), (G, dk) = vs[:lead_dims], vs[-2:], qs[-2:]
-    dtype, dev = q.dtype, q.get_device()
+    H, dv, G, dk = vs[-2], vs[-1], qs[-2], qs[-1]
     if k.shape != qs or G < 1 or H % G:
         raise ValueError("q and k must share a shape [.., G, dk], G dividing H = %d" % H)
     if k.dtype != dtype or v.dtype != dtype or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k and v must be of one dtype and on one device")
-    ldq, ldk, ldv = _row_ld("q", q, lead, G * dk), _row_ld("k", k, lead, G * dk), _row_ld("v", v, lead, H * dv)
-    _check_like("log_alpha", log_alpha, lead + (H,), q)
-    _check_like("dt", dt, lead + (H,), q)
-    _check_f32("skip", skip, (H,), q)
+    hs = vs[:-1]
+    lead = hs[:-1]
+    if qs[:-2] != lead:
+        raise ValueError("q must have leading dimensions %s, got %s" % (tuple(lead), tuple(qs)))
+    ldq = G * dk if q.is_contiguous() else _row_ld("q", q, lead_dims, G * dk)
+    ldk = G * dk if k.is_contiguous() else _row_ld("k", k, lead_dims, G * dk)
+    ldv = H * dv if v.is_contiguous() else _row_ld("v", v, lead_dims, H * dv)
+    _check_like("log_alpha", log_alpha, hs, dtype, dev)
+    _check_like("dt", dt, hs, dtype, dev)
+    if skip is not None:
+        _check_f32("skip", skip, (H,), dev)
     if cu_seqlens is None:
-        B, T = (lead[0], 1) if lead_dims == 1 else lead
+        B, T = (vs[0], 1) if lead_dims == 1 else lead
     else:
-        B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
+        B, T = _check_cu(cu_seqlens, vs[0]), vs[0]
         if cu_seqlens.get_device() != dev:
             raise ValueError("cu_seqlens must be on %s" % q.device)
-    return lead, B, T, H, G, dk, dv, ldq, ldk, ldv
+    return hs, dev, B, T, H, G, dk, dv, ldq, ldk, ldv
 
 
 def _like_rows(t, ld):
     """An empty tensor with t's shape and row distance."""
-    return t.new_empty(t.shape) if ld == t.shape[-2] * t.shape[-1] else t.new_empty_strided(t.shape, t.stride())
+    return _empty_as(t) if ld == t.shape[-2] * t.shape[-1] else t.new_empty_strided(t.shape, t.stride())
 
 
 def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True, save_states=False, cu_seqlens=None,
@@ -791,11 +805,13 @@ def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True,
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return ssm_fwd(q, k, v, log_alpha, dt, skip, S0, output_final_state, save_states, cu_seqlens, stream)
-    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
+    _, dev, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
     code, packed = _dtype_code(q), cu_seqlens is not None
-    _check_f32("S0", S0, (B, H, dk, dv), q)
-    o = v.new_empty(lead + (H, dv))
-    S_T = v.new_empty((B, H, dk, dv), dtype=torch.float32) if output_final_state else None
+    if S0 is not None:
+        _check_f32("S0", S0, (B, H, dk, dv), dev)
+    o, S_T = _empty_as(v), None
+    if output_final_state:
+        S_T = v.new_empty((B, H, dk, dv), dtype=torch.float32) if S0 is None else torch.empty_like(S0)
     states = None
     if save_states:
         states = v.new_empty(gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed), dtype=torch.uint8)
@@ -818,22 +834,26 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return ssm_bwd(q, k, v, log_alpha, dt, dO, skip, S0, dS_T, states, need_dS0, cu_seqlens, into, stream)
-    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
+    hs, dev, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
     code, packed = _dtype_code(q), cu_seqlens is not None
-    _check_f32("S0", S0, (B, H, dk, dv), q)
-    _check_f32("dS_T", dS_T, (B, H, dk, dv), q)
-    _check_like("dO", dO, lead + (H, dv), q)
-    if states is not None and (states.dtype != torch.uint8 or states.get_device() != q.get_device() or
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _check_f32(name, t, (B, H, dk, dv), dev)
+    _check_like("dO", dO, v.shape, q.dtype, dev)
+    if states is not None and (states.dtype != torch.uint8 or states.get_device() != dev or
                                not states.is_contiguous() or
                                states.numel() != gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed)):
         raise ValueError("states must be what ssm_fwd(..., save_states=True) returned for these sizes")
     for name, t, x, ld, w in zip(("dq", "dk", "dv"), into or (), (q, k, v), (ldq, ldk, ldv), (G * dk, G * dk, H * dv)):
-        if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device() or _row_ld(name, t, lead, w) != ld:
+        if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != dev or _row_ld(name, t, len(hs) - 1, w) != ld:
             raise ValueError("%s must have its input's shape, dtype and row stride" % name)
     dq, dk_, dv_ = into or (_like_rows(q, ldq), _like_rows(k, ldk), _like_rows(v, ldv))
     g = {"dq": dq, "dk": dk_, "dv": dv_, "dlog_alpha": torch.empty_like(log_alpha), "ddt": torch.empty_like(dt),
          "dskip": None if skip is None else torch.empty_like(skip),
-         "dS0": q.new_empty((B, H, dk, dv), dtype=torch.float32) if need_dS0 else None}
+         "dS0": None}
+    if need_dS0:
+        like = S0 if S0 is not None else dS_T
+        g["dS0"] = q.new_empty((B, H, dk, dv), dtype=torch.float32) if like is None else torch.empty_like(like)
     nws = load().gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, code, packed, states is not None)
     ws = _scratch(nws, q, stream)
     _raise(load().gdn2_ssm_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
@@ -851,9 +871,9 @@ def ssm_step(q, k, v, log_alpha, dt, S, skip=None, stream=None):
         import torch
         with torch.cuda.device(q.device):
             return ssm_step(q, k, v, log_alpha, dt, S, skip, stream)
-    lead, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, None, 1)
-    _check_f32("S", S, (B, H, dk, dv), q)
-    o = v.new_empty((B, H, dv))
+    _, dev, B, _, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, None, 1)
+    _check_f32("S", S, (B, H, dk, dv), dev)
+    o = _empty_as(v)
     _raise(load().gdn2_ssm_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
                                 S.data_ptr(), o.data_ptr(), ldq, ldk, ldv, B, H, G, dk, dv, _dtype_code(q),
                                 _raw_stream(q, stream)), "gdn2_ssm_step")
@@ -863,29 +883,31 @@ def ssm_step(q, k, v, log_alpha, dt, S, skip=None, stream=None):
 def _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, cu_seqlens, lead_dims):
     if cu_seqlens is not None:
         lead_dims = 1
-    xs = x.shape
+    xs, dtype, dev = x.shape, x.dtype, x.get_device()
     if len(xs) != lead_dims + 1 or W.dim() != 2:
         raise ValueError("x must be %s and W [C, K]" % ("[rows, C]" if lead_dims == 1 else "[B, T, C]"))
     lead, C, K = xs[:lead_dims], xs[-1], W.shape[1]
-    _check_f32("W", W, (C, K), x)
-    _check_f32("bias", bias, (C,), x)
+    _check_f32("W", W, (C, K), dev)
+    if bias is not None:
+        _check_f32("bias", bias, (C,), dev)
     H, ldt = 0, 0
     if xdt is not None:
         H = xdt.shape[-1]
-        if xdt.dtype != x.dtype or xdt.get_device() != x.get_device() or xdt.dim() != lead_dims + 1 or A_log is None:
-            raise ValueError("xdt must be a %s tensor %s + (H,) on %s, with A_log" % (x.dtype, tuple(lead), x.device))
-        ldt = _row_ld("xdt", xdt, lead, H)
-        _check_f32("dt_bias", dt_bias, (H,), x)
-        _check_f32("A_log", A_log, (H,), x)
+        if xdt.dtype != dtype or xdt.get_device() != dev or xdt.shape[:-1] != lead or A_log is None:
+            raise ValueError("xdt must be a %s tensor %s + (H,) on %s, with A_log" % (dtype, tuple(lead), x.device))
+        ldt = _row_ld("xdt", xdt, lead_dims, H)
+        if dt_bias is not None:
+            _check_f32("dt_bias", dt_bias, (H,), dev)
+        _check_f32("A_log", A_log, (H,), dev)
     if cu_seqlens is None:
-        B, T = (lead[0], 1) if lead_dims == 1 else lead
+        B, T = (xs[0], 1) if lead_dims == 1 else lead
     else:
-        B, T = _check_cu(cu_seqlens, lead[0]), lead[0]
-        if cu_seqlens.get_device() != x.get_device():
+        B, T = _check_cu(cu_seqlens, xs[0]), xs[0]
+        if cu_seqlens.get_device() != dev:
             raise ValueError("cu_seqlens must be on %s" % x.device)
     if window is not None:
-        _check_like("the window", window, (B, K - 1, C), x)
-    return lead, B, T, C, K, H, _row_ld("x", x, lead, C), ldt
+        _check_like("the window", window, (B, K - 1, C), dtype, dev)
+    return dev, B, T, C, K, H, _row_ld("x", x, lead_dims, C), ldt
 
 
 def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False, cu_seqlens=None, stream=None):
@@ -899,10 +921,12 @@ def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False
         import torch
         with torch.cuda.device(x.device):
             return ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init, output_window, cu_seqlens, stream)
-    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
-    y = x.new_empty(lead + (C,))
-    dt, la = (x.new_empty(lead + (H,)), x.new_empty(lead + (H,))) if H else (None, None)
-    window = x.new_empty((B, K - 1, C)) if output_window else None
+    _, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
+    y = _empty_as(x)
+    dt, la = (_empty_as(xdt), _empty_as(xdt)) if H else (None, None)
+    window = None
+    if output_window:
+        window = x.new_empty((B, K - 1, C)) if init is None else _empty_as(init)
     _raise(load().gdn2_ssm_prologue_fwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
                                         _at(init), y.data_ptr(), _at(dt), _at(la), _at(window), _at(cu_seqlens), ldx, ldt,
                                         B, T, C, H, _dtype_code(x), _raw_stream(x, stream)), "gdn2_ssm_prologue_fwd")
@@ -917,16 +941,16 @@ def ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt=None, dlog_alpha=N
     if _elsewhere(x):
         with torch.cuda.device(x.device):
             return ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt, dlog_alpha, init, cu_seqlens, stream)
-    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
-    for name, t, w in (("dy", dy, C), ("ddt", ddt, H), ("dlog_alpha", dlog_alpha, H)):
-        if w:
+    dev, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
+    for name, t, like in (("dy", dy, x), ("ddt", ddt, xdt), ("dlog_alpha", dlog_alpha, xdt)):
+        if like is not None:
             if t is None:
                 raise ValueError("%s is missing" % name)
-            _check_like(name, t, lead + (w,), x)
+            _check_like(name, t, like.shape, x.dtype, dev)
     e = torch.empty_like
-    g = {"dx": x.new_empty(lead + (C,)), "dW": e(W), "dbias": None if bias is None else e(bias),
+    g = {"dx": _empty_as(x), "dW": e(W), "dbias": None if bias is None else e(bias),
          "dinit": None if init is None else e(init), "ddt_bias": e(dt_bias) if H and dt_bias is not None else None,
-         "dA_log": e(A_log) if H else None, "dxdt": x.new_empty(lead + (H,)) if H else None}
+         "dA_log": e(A_log) if H else None, "dxdt": _empty_as(xdt) if H else None}
     nws = load().gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, cu_seqlens is not None)
     ws = _scratch(nws, x, stream)
     _raise(load().gdn2_ssm_prologue_bwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
@@ -944,9 +968,9 @@ def ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream=None):
         import torch
         with torch.cuda.device(x.device):
             return ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream)
-    lead, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, None, 1)
-    y = x.new_empty((B, C))
-    dt, la = (x.new_empty((B, H)), x.new_empty((B, H))) if H else (None, None)
+    _, B, _, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, None, 1)
+    y = _empty_as(x)
+    dt, la = (_empty_as(xdt), _empty_as(xdt)) if H else (None, None)
     _raise(load().gdn2_ssm_prologue_step(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
                                          _at(window), y.data_ptr(), _at(dt), _at(la), ldx, ldt, B, C, H, _dtype_code(x),
                                          _raw_stream(x, stream)), "gdn2_ssm_prologue_step")

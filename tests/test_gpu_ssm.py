@@ -678,3 +678,58 @@ def test_batches_and_sequences_of_nothing():
         assert torch.all(gp["dW"] == 0) and torch.all(gp["dA_log"] == 0) and torch.all(gp["dinit"] == 0)
     assert g.ssm_step(e(0, 1, 64), e(0, 1, 64), e(0, 2, 64), e(0, 2), e(0, 2), e(0, 2, 64, 64)).shape == (0, 2, 64)
     assert g.gdn2_get_device_status() == 0
+
+
+def test_arguments_are_checked():
+    """What the tensors must be: each of these is refused before anything is launched."""
+    import gated_delta_rule_gdn2_b200 as g
+    B, T, H, G, dk, dv = 2, 6, 4, 2, 64, 64
+    d = dev(make(B, T, H, G, dk, dv, "bf16", seed=81), "bf16")
+    d.update(W=torch.randn(dv, 4, device="cuda"), A=torch.randn(H, device="cuda"), cu=cu_of((2, 4)))
+    x, win = d["v"][:, :, 0].contiguous(), torch.zeros(B, 3, dv, dtype=torch.bfloat16, device="cuda")
+
+    def fwd(**kw):
+        a = {**d, **kw}
+        return g.ssm_fwd(*[a[n] for n in ("q", "k", "v", "la", "dt")], skip=a["skip"], S0=a["S0"], cu_seqlens=kw.get("cu"))
+
+    def bwd(**kw):
+        a = {**d, **kw}
+        return g.ssm_bwd(*[a[n] for n in ("q", "k", "v", "la", "dt", "dO")], skip=a["skip"], S0=a["S0"], dS_T=a["dS_T"],
+                         states=kw.get("states"), into=kw.get("into"))
+
+    def step(**kw):
+        a = {**{n: t[:, 0].contiguous() for n, t in d.items() if n in ("q", "k", "v", "la", "dt")}, "S": d["S0"].clone(), **kw}
+        return g.ssm_step(*[a[n] for n in ("q", "k", "v", "la", "dt", "S")], skip=d["skip"])
+
+    def pro(f=g.ssm_prologue, **kw):
+        a = {"x": x, "W": d["W"], "bias": None, "xdt": d["dt"], "dt_bias": None, "A": d["A"], **kw}
+        more = {n: a[n] for n in ("init", "cu_seqlens", "ddt", "dlog_alpha") if n in a}
+        pos = [a[n] for n in ("dy",) if n in a]
+        return f(*[a[n] for n in ("x", "W", "bias", "xdt", "dt_bias", "A")], *pos, **more)
+
+    for f in (fwd, bwd, step, pro):
+        if f is not bwd:
+            f()
+    bad = [
+        (fwd, dict(q=d["q"].float())), (fwd, dict(k=d["k"][:, :5])), (fwd, dict(k=d["k"][..., :1, :])),
+        (fwd, dict(q=d["q"][:, :, :, ::2], k=d["k"][:, :, :, ::2])), (fwd, dict(v=d["v"].transpose(1, 2))),
+        (fwd, dict(la=d["la"].float())), (fwd, dict(la=d["la"].transpose(0, 1))), (fwd, dict(dt=d["dt"][..., :3])),
+        (fwd, dict(skip=d["skip"].bfloat16())), (fwd, dict(skip=d["skip"][:2])), (fwd, dict(S0=d["S0"][:1])),
+        (fwd, dict(S0=d["S0"].transpose(2, 3))), (fwd, dict(cu=cu_of((2, 4)))), (fwd, dict(q=d["q"].cpu())),
+        (fwd, dict(la=d["la"].cpu())), (fwd, dict(v=d["v"][:, :5])), (fwd, dict(v=d["v"][:1].expand(2, -1, -1, -1))),
+        (bwd, dict(dO=d["dO"].float())), (bwd, dict(dO=d["dO"][:, :5])), (bwd, dict(dS_T=d["dS_T"].bfloat16())),
+        (bwd, dict(states=torch.zeros(16, dtype=torch.uint8, device="cuda"))),
+        (bwd, dict(into=(d["q"].float(), d["k"], d["v"]))), (bwd, dict(into=(d["q"], d["k"], d["v"][:, :5]))),
+        (step, dict(S=d["S0"].bfloat16())), (step, dict(S=d["S0"][:1])), (step, dict(la=d["la"])),
+        (pro, dict(W=d["W"].bfloat16())), (pro, dict(W=d["W"][:8])), (pro, dict(bias=d["A"])), (pro, dict(A=None)),
+        (pro, dict(xdt=d["dt"][:, :5])), (pro, dict(xdt=d["dt"].float())), (pro, dict(init=win[:, :2])),
+        (pro, dict(x=x.transpose(0, 1))), (pro, dict(dt_bias=d["A"][:2])),
+        (pro, dict(f=g.ssm_prologue_bwd, dy=x)), (pro, dict(f=g.ssm_prologue_bwd, dy=x[:, :5], ddt=d["dt"], dlog_alpha=d["dt"])),
+    ]
+    for i, (f, kw) in enumerate(bad):
+        with pytest.raises((ValueError, g.Gdn2Error)):
+            f(**kw)
+            pytest.fail("case %d (%s) was taken" % (i, list(kw)))
+    with pytest.raises(TypeError):
+        fwd(q=d["q"].half(), k=d["k"].half(), v=d["v"].half(), la=d["la"].half(), dt=d["dt"].half())
+    assert g.gdn2_get_device_status() == 0
