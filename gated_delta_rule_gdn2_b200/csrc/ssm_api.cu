@@ -91,7 +91,8 @@ Plan plan(const void *cu, int B, int T, int H, int G, int dk, int dv, int dtype,
         // heads of a group in one block after another, unless the blocks then
         // leave a fifth of the GPU idle (several runs' sums cost a pass over
         // dq and dk in fp32)
-        const double sms = device_sm_count();
+        // (two of the fp32 kernel's blocks share an SM at dk = dv = 64)
+        const double sms = device_sm_count() * (dtype == GDN2_FP32 && dk + dv == 128 ? 2 : 1);
         auto cost = [&](int n) { return std::ceil(slots * G * n / sms) * ((hpg + n - 1) / n); };
         for (int n = 2; n <= hpg; n *= 2)
             if (cost(n) < 0.8 * cost(p.splits)) p.splits = n;
