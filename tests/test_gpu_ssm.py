@@ -733,3 +733,32 @@ def test_arguments_are_checked():
     with pytest.raises(TypeError):
         fwd(q=d["q"].half(), k=d["k"].half(), v=d["v"].half(), la=d["la"].half(), dt=d["dt"].half())
     assert g.gdn2_get_device_status() == 0
+
+
+@pytest.mark.parametrize("B,H,bad", [(6, 32, False), (64, 4, False), (65, 4, False), (64, 4, True)])
+def test_packed_batches_of_many_blocks(B, H, bad):
+    """More blocks than SMs, which take the sequences by length: bit for bit
+    each sequence alone, equal lengths and empty ones among them, and beside a
+    sequence whose offsets are out of range."""
+    import gated_delta_rule_gdn2_b200 as g
+    lens = [(0, 130, 130, 17, 260, 1, 64)[i % 7] for i in range(B)]
+    T = sum(lens)
+    d = dev(make(B, T, H, 2, 64, 64, "bf16", lens=lens, seed=91), "bf16")
+    names = ("q", "k", "v", "la", "dt")
+    cu = cu_of(lens)
+    if bad:
+        cu[-1] = T + 1
+    a = [d[n] for n in names]
+    o, ST, st = g.ssm_fwd(*a, skip=d["skip"], S0=d["S0"], save_states=True, cu_seqlens=cu)
+    gr = g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], states=st, cu_seqlens=cu)
+    assert g.gdn2_get_device_status() == (-1 if bad else 0)
+    ends = np.cumsum([0] + lens)
+    for b in range(B - bad):
+        if 14 < b < B - 8:  # (the pattern repeats)
+            continue
+        s, one = slice(ends[b], ends[b + 1]), slice(b, b + 1)
+        x = [t[None, s].contiguous() for t in a]
+        ob, Sb = g.ssm_fwd(*x, skip=d["skip"], S0=d["S0"][one])
+        gb = g.ssm_bwd(*x, d["dO"][None, s].contiguous(), skip=d["skip"], S0=d["S0"][one], dS_T=d["dS_T"][one])
+        for got, want in ((o[s], ob[0]), (ST[b], Sb[0]), (gr["dv"][s], gb["dv"][0]), (gr["dS0"][b], gb["dS0"][0])):
+            assert torch.equal(got, want), b
