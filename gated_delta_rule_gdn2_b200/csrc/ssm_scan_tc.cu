@@ -274,10 +274,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                         tc::bulk_commit();
                     }
                 }
-                if (m > 0 && more) {  // the chunk before: its q, k and o are out of the way
+                if (m > 0) {
+                    // the chunk before: its o has been read out of its tile, which this chunk's
+                    // o goes to once M v is done (N < P: every chunk has the one tile), or the next q
                     if (elect()) tc::bulk_wait_read();
                     __syncwarp();
-                    load_qk(m + 1);
+                    if (more) load_qk(m + 1);
                 }
                 if (!(ok = wait(&r_m, ph) && wait(&r_y2, ph))) break;
                 tc::fence_after();
