@@ -675,6 +675,11 @@ def chunk_fwd_gated(q, k, v, log_alpha, b, w, g, gamma, S0=None, output_final_st
 # A single token's call is over in microseconds, so these checks are written to
 # cost little: shapes and strides are read once, and contiguous tensors take a
 # short way.
+#
+# stream= (a torch stream or a raw handle): the call runs, and allocates what it
+# returns, as if that stream were the current one.  The caller orders it behind
+# the making of its inputs, keeps these alive until it has run, and orders what
+# reads its outputs on another stream behind it.
 
 
 def _elsewhere(t):
@@ -687,23 +692,33 @@ def _elsewhere(t):
     return i != torch._C._cuda_getDevice()
 
 
-def _raw_stream(t, stream):
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _scratch(n, like, stream):
-    """n bytes of workspace on like's device (None for none).  It belongs to
-    the current stream; for a call on another it is recorded there."""
+def _there(fn, t, stream, *args, **kw):
+    """fn(*args, **kw) with t's device current and, where one is given, `stream`
+    (a torch stream or a handle) as its current stream.  What the call allocates
+    then comes from that stream's own memory pool: a block of the calling
+    stream's pool may still be in use by work that stream has pending, and
+    nothing orders the call behind it."""
     import torch
-    if not n:
-        return None
-    ws = like.new_empty(n, dtype=torch.uint8)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
-    return ws
+    with torch.cuda.device(t.device):
+        if stream is None:
+            return fn(*args, **kw)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        if stream.device != t.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+
+def _raw_stream(t):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _scratch(n, like):
+    """n bytes of workspace on like's device (None for none), of the current stream's pool."""
+    import torch
+    return like.new_empty(n, dtype=torch.uint8) if n else None
 
 
 def _at(t):
@@ -801,10 +816,9 @@ def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True,
     q, k, v may be views with a longer row stride.  Packed: [rows, ..] tensors
     and cu_seqlens (B + 1 int32 offsets on the device).  With save_states=True
     returns (o, S_T, states) for ssm_bwd(..., states=states)."""
+    if _elsewhere(q) or stream is not None:
+        return _there(ssm_fwd, q, stream, q, k, v, log_alpha, dt, skip, S0, output_final_state, save_states, cu_seqlens)
     import torch
-    if _elsewhere(q):
-        with torch.cuda.device(q.device):
-            return ssm_fwd(q, k, v, log_alpha, dt, skip, S0, output_final_state, save_states, cu_seqlens, stream)
     _, dev, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
     code, packed = _dtype_code(q), cu_seqlens is not None
     if S0 is not None:
@@ -816,10 +830,10 @@ def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True,
     if save_states:
         states = v.new_empty(gdn2_ssm_states_bytes(B, T, H, dk, dv, code, packed), dtype=torch.uint8)
     nws = load().gdn2_ssm_fwd_workspace(B, T, H, G, dk, dv, code, packed)
-    ws = _scratch(nws, q, stream)
+    ws = _scratch(nws, q)
     _raise(load().gdn2_ssm_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
                                _at(S0), o.data_ptr(), _at(S_T), _at(states), _at(cu_seqlens), ldq, ldk, ldv, B, T, H, G,
-                               dk, dv, code, _at(ws), nws, _raw_stream(q, stream)), "gdn2_ssm_fwd")
+                               dk, dv, code, _at(ws), nws, _raw_stream(q)), "gdn2_ssm_fwd")
     return (o, S_T, states) if save_states else (o, S_T)
 
 
@@ -830,10 +844,9 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
     skips forming them anew.  dq, dk, dv have their input's strides; `into`
     (dq, dk, dv) gives the tensors to write them to, such as views of the
     prologue's dy."""
+    if _elsewhere(q) or stream is not None:
+        return _there(ssm_bwd, q, stream, q, k, v, log_alpha, dt, dO, skip, S0, dS_T, states, need_dS0, cu_seqlens, into)
     import torch
-    if _elsewhere(q):
-        with torch.cuda.device(q.device):
-            return ssm_bwd(q, k, v, log_alpha, dt, dO, skip, S0, dS_T, states, need_dS0, cu_seqlens, into, stream)
     hs, dev, B, T, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, 2)
     code, packed = _dtype_code(q), cu_seqlens is not None
     for name, t in (("S0", S0), ("dS_T", dS_T)):
@@ -855,28 +868,26 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
         like = S0 if S0 is not None else dS_T
         g["dS0"] = q.new_empty((B, H, dk, dv), dtype=torch.float32) if like is None else torch.empty_like(like)
     nws = load().gdn2_ssm_bwd_workspace(B, T, H, G, dk, dv, code, packed, states is not None)
-    ws = _scratch(nws, q, stream)
+    ws = _scratch(nws, q)
     _raise(load().gdn2_ssm_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
                                _at(S0), dO.data_ptr(), _at(dS_T), _at(states), dq.data_ptr(), dk_.data_ptr(),
                                dv_.data_ptr(), g["dlog_alpha"].data_ptr(), g["ddt"].data_ptr(), _at(g["dskip"]),
                                _at(g["dS0"]), _at(cu_seqlens), ldq, ldk, ldv, B, T, H, G, dk, dv, code, _at(ws), nws,
-                               _raw_stream(q, stream)), "gdn2_ssm_bwd")
+                               _raw_stream(q)), "gdn2_ssm_bwd")
     return g
 
 
 def ssm_step(q, k, v, log_alpha, dt, S, skip=None, stream=None):
     """o = one token of the scan: v [B, H, dv], q, k [B, G, dk], log_alpha, dt
     [B, H]; S fp32 [B, H, dk, dv] updated in place."""
-    if _elsewhere(q):
-        import torch
-        with torch.cuda.device(q.device):
-            return ssm_step(q, k, v, log_alpha, dt, S, skip, stream)
+    if _elsewhere(q) or stream is not None:
+        return _there(ssm_step, q, stream, q, k, v, log_alpha, dt, S, skip)
     _, dev, B, _, H, G, dk, dv, ldq, ldk, ldv = _scan_sizes(q, k, v, log_alpha, dt, skip, None, 1)
     _check_f32("S", S, (B, H, dk, dv), dev)
     o = _empty_as(v)
     _raise(load().gdn2_ssm_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), dt.data_ptr(), _at(skip),
                                 S.data_ptr(), o.data_ptr(), ldq, ldk, ldv, B, H, G, dk, dv, _dtype_code(q),
-                                _raw_stream(q, stream)), "gdn2_ssm_step")
+                                _raw_stream(q)), "gdn2_ssm_step")
     return o
 
 
@@ -917,10 +928,8 @@ def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False
     before each sequence (None: zeros); window: those before its next token
     (None without output_window).  x and xdt may be slices of wider rows.
     Packed: [rows, ..] and cu_seqlens."""
-    if _elsewhere(x):
-        import torch
-        with torch.cuda.device(x.device):
-            return ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init, output_window, cu_seqlens, stream)
+    if _elsewhere(x) or stream is not None:
+        return _there(ssm_prologue, x, stream, x, W, bias, xdt, dt_bias, A_log, init, output_window, cu_seqlens)
     _, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
     y = _empty_as(x)
     dt, la = (_empty_as(xdt), _empty_as(xdt)) if H else (None, None)
@@ -929,7 +938,7 @@ def ssm_prologue(x, W, bias, xdt, dt_bias, A_log, init=None, output_window=False
         window = x.new_empty((B, K - 1, C)) if init is None else _empty_as(init)
     _raise(load().gdn2_ssm_prologue_fwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
                                         _at(init), y.data_ptr(), _at(dt), _at(la), _at(window), _at(cu_seqlens), ldx, ldt,
-                                        B, T, C, H, _dtype_code(x), _raw_stream(x, stream)), "gdn2_ssm_prologue_fwd")
+                                        B, T, C, H, _dtype_code(x), _raw_stream(x)), "gdn2_ssm_prologue_fwd")
     return y, dt, la, window
 
 
@@ -937,10 +946,9 @@ def ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt=None, dlog_alpha=N
                      stream=None):
     """Gradients of ssm_prologue from dy, ddt and dlog_alpha: dx, dW, dbias,
     dxdt, ddt_bias, dA_log and, with init, dinit (None for what was not given)."""
+    if _elsewhere(x) or stream is not None:
+        return _there(ssm_prologue_bwd, x, stream, x, W, bias, xdt, dt_bias, A_log, dy, ddt, dlog_alpha, init, cu_seqlens)
     import torch
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
-            return ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt, dlog_alpha, init, cu_seqlens, stream)
     dev, B, T, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, init, cu_seqlens, 2)
     for name, t, like in (("dy", dy, x), ("ddt", ddt, xdt), ("dlog_alpha", dlog_alpha, xdt)):
         if like is not None:
@@ -952,26 +960,24 @@ def ssm_prologue_bwd(x, W, bias, xdt, dt_bias, A_log, dy, ddt=None, dlog_alpha=N
          "dinit": None if init is None else e(init), "ddt_bias": e(dt_bias) if H and dt_bias is not None else None,
          "dA_log": e(A_log) if H else None, "dxdt": _empty_as(xdt) if H else None}
     nws = load().gdn2_ssm_prologue_bwd_workspace(B, T, C, K, H, cu_seqlens is not None)
-    ws = _scratch(nws, x, stream)
+    ws = _scratch(nws, x)
     _raise(load().gdn2_ssm_prologue_bwd(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
                                         _at(init), dy.data_ptr(), _at(ddt), _at(dlog_alpha), g["dx"].data_ptr(),
                                         g["dW"].data_ptr(), _at(g["dbias"]), _at(g["dxdt"]), _at(g["ddt_bias"]),
                                         _at(g["dA_log"]), _at(g["dinit"]), _at(cu_seqlens), ldx, ldt, B, T, C, H,
-                                        _dtype_code(x), _at(ws), nws, _raw_stream(x, stream)), "gdn2_ssm_prologue_bwd")
+                                        _dtype_code(x), _at(ws), nws, _raw_stream(x)), "gdn2_ssm_prologue_bwd")
     return g
 
 
 def ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream=None):
     """(y, dt, log_alpha) of one token per sequence: x [B, C], xdt [B, H]
     (None: only y); window [B, K-1, C] updated in place."""
-    if _elsewhere(x):
-        import torch
-        with torch.cuda.device(x.device):
-            return ssm_prologue_step(x, W, bias, xdt, dt_bias, A_log, window, stream)
+    if _elsewhere(x) or stream is not None:
+        return _there(ssm_prologue_step, x, stream, x, W, bias, xdt, dt_bias, A_log, window)
     _, B, _, C, K, H, ldx, ldt = _prologue_sizes(x, W, bias, xdt, dt_bias, A_log, window, None, 1)
     y = _empty_as(x)
     dt, la = (_empty_as(xdt), _empty_as(xdt)) if H else (None, None)
     _raise(load().gdn2_ssm_prologue_step(x.data_ptr(), W.data_ptr(), _at(bias), K, _at(xdt), _at(dt_bias), _at(A_log),
                                          _at(window), y.data_ptr(), _at(dt), _at(la), ldx, ldt, B, C, H, _dtype_code(x),
-                                         _raw_stream(x, stream)), "gdn2_ssm_prologue_step")
+                                         _raw_stream(x)), "gdn2_ssm_prologue_step")
     return y, dt, la

@@ -1,0 +1,97 @@
+"""Calls given a stream that is not the current one: what they allocate belongs
+to that stream, so that work which the calling stream has pending cannot be
+using the same memory."""
+import types
+
+import pytest
+import torch
+
+from test_gpu_ssm import dev, make, pro_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def tensors(x):
+    if x is None:
+        return []
+    if isinstance(x, torch.Tensor):
+        return [x]
+    return [t for y in (x.values() if isinstance(x, dict) else x) for t in tensors(y)]
+
+
+def pool_of(t):
+    """The stream whose memory pool holds t."""
+    at = t.untyped_storage().data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+def ssm_calls(g):
+    d = dev(make(2, 300, 4, 2, 128, 64, "bf16", seed=111), "bf16")
+    a = [d[n] for n in ("q", "k", "v", "la", "dt")]
+    one = [t[:, 0].contiguous() for t in a]
+    _, _, p = pro_inputs((2, 70), 2, 64, 4, 3, "bf16", True, seed=112)
+    w = [p[n] for n in ("W", "bias", "xdt", "dt_bias", "A_log")]
+    first = [p["W"], p["bias"], p["xdt"][:, 0], p["dt_bias"], p["A_log"]]
+    states = g.ssm_fwd(*a, skip=d["skip"], S0=d["S0"], save_states=True)[2]
+    return {
+        "ssm_fwd": lambda **k: g.ssm_fwd(*a, skip=d["skip"], S0=d["S0"], save_states=True, **k),
+        "ssm_bwd": lambda **k: g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], states=states, **k),
+        "ssm_bwd, states anew": lambda **k: g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], **k),
+        "ssm_step": lambda **k: g.ssm_step(*one, d["S0"].clone(), skip=d["skip"], **k),
+        "ssm_prologue": lambda **k: g.ssm_prologue(p["x"], *w, init=p["init"], output_window=True, **k),
+        "ssm_prologue_bwd": lambda **k: g.ssm_prologue_bwd(p["x"], *w, p["dy"], p["ddt"], p["dla"], init=p["init"], **k),
+        "ssm_prologue_step": lambda **k: g.ssm_prologue_step(p["x"][:, 0], *first, p["init"].clone(), **k),
+    }
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_and_workspace_are_of_the_streams_pool(handle, monkeypatch):
+    import gated_delta_rule_gdn2_b200 as g
+    from gated_delta_rule_gdn2_b200 import binding
+    side, work = torch.cuda.Stream(), []
+    scratch = binding._scratch
+
+    def spy(*args):
+        work.append(scratch(*args))
+        return work[-1]
+
+    monkeypatch.setattr(binding, "_scratch", spy)
+    for name, call in ssm_calls(g).items():
+        del work[:]
+        torch.cuda.synchronize()
+        out = tensors(call(stream=side.cuda_stream if handle else side))
+        torch.cuda.synchronize()
+        assert out
+        for t in out + tensors(work):
+            assert not t.numel() or pool_of(t) == side.cuda_stream, name
+    assert torch.cuda.current_stream() != side and g.gdn2_get_device_status() == 0
+
+
+def test_a_call_elsewhere_right_behind_one_here():
+    """Without a wait between them, as often as not with what the call before
+    has just given back."""
+    import gated_delta_rule_gdn2_b200 as g
+    calls = ssm_calls(g)
+    del calls["ssm_step"], calls["ssm_prologue_step"]  # (their states are made on the current stream)
+    want = {n: tensors(f()) for n, f in calls.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for n, f in calls.items():
+            here = tensors(f())
+            there = tensors(f(stream=side))
+            f()
+            torch.cuda.synchronize()
+            for x, y, z in zip(want[n], here, there):
+                assert torch.equal(x, y) and torch.equal(x, z), n
+
+
+def test_a_stream_of_another_device_is_refused():
+    import gated_delta_rule_gdn2_b200 as g
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    for n, f in ssm_calls(g).items():
+        with pytest.raises(ValueError):
+            f(stream=other)
