@@ -11,6 +11,7 @@ library's CUDA kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -372,6 +373,44 @@ def gdn2_ssm_prologue_step(x, W, bias, K, xdt, dt_bias, A_log, window, y, dt, lo
 
 # --------------------------------------------------------------------------
 # torch conveniences
+#
+# stream= (a torch stream or a raw handle): the call runs, and allocates what it
+# returns, as if that stream were the current one.  The caller orders it behind
+# the making of its inputs, keeps these alive until it has run, and orders what
+# reads its outputs on another stream behind it.
+
+
+def _there(fn, t, stream, *args, **kw):
+    """fn(*args, **kw) with t's device current and, where one is given, `stream`
+    (a torch stream or a handle) as its current stream.  What the call allocates
+    then comes from that stream's own memory pool: a block of the calling
+    stream's pool may still be in use by work that stream has pending, and
+    nothing orders the call behind it."""
+    import torch
+    with torch.cuda.device(t.device):
+        if stream is None:
+            return fn(*args, **kw)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        if stream.device != t.device:
+            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+
+def _on_stream(fn):
+    """fn, whose last argument is `stream`, called with that stream current where one is given."""
+    at = fn.__code__.co_argcount - 1
+    first = fn.__code__.co_varnames[0]
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = kw.pop("stream", None) if len(args) <= at else args[at]
+        if stream is None:
+            return fn(*args, **kw)
+        return _there(fn, args[0] if args else kw[first], stream, *args[:at], **kw)
+
+    return call
 
 
 def _dtype_code(t):
@@ -401,6 +440,7 @@ def _raise(st, what):
         raise Gdn2Error(st, what)
 
 
+@_on_stream
 def chunk_fwd(q, k, v, log_alpha, b, w, S0=None, output_final_state=True, save_states=False, stream=None):
     """o, S_T = chunk_fwd(...) for token tensors [B,T,H,D] (bf16 or fp32).
 
@@ -426,6 +466,7 @@ def chunk_fwd(q, k, v, log_alpha, b, w, S0=None, output_final_state=True, save_s
     return o, S_T, states
 
 
+@_on_stream
 def decode_step(q, k, v, log_alpha, b, w, S, stream=None):
     """o = decode_step(...): tokens [B,H,D]; S [B,H,dk,dv] fp32 updated in place."""
     import torch
@@ -440,6 +481,7 @@ def decode_step(q, k, v, log_alpha, b, w, S, stream=None):
     return o
 
 
+@_on_stream
 def chunk_bwd(q, k, v, log_alpha, b, w, S0, dO, dS_T=None, need_dS0=True, states=None, stream=None):
     """Gradients (dq, dk, dv, dlog_alpha, db, dw, dS0) of gdn2_chunk_fwd.
 
@@ -475,6 +517,7 @@ def _check_cu(cu_seqlens, total_T):
     return cu_seqlens.numel() - 1
 
 
+@_on_stream
 def chunk_fwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0=None, output_final_state=True, save_states=False,
                      stream=None):
     """o, S_T = chunk_fwd_varlen(...) for packed token tensors [total_T, H, D]
@@ -503,6 +546,7 @@ def chunk_fwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0=None, output_final
     return o, S_T, states
 
 
+@_on_stream
 def chunk_bwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0, dO, dS_T=None, need_dS0=True, states=None,
                      stream=None):
     """Gradients of chunk_fwd_varlen: dq, dk, dv, dlog_alpha, db, dw as [total_T, H, D], dS0 [N, H, dk, dv]."""
@@ -545,6 +589,7 @@ def _check_reduced(q, k, v, log_alpha, beta, mode, lead_dims):
         raise ValueError("shapes: q, k %s; log_alpha %s; beta %s" % (tuple(q.shape), tuple(want_la), lead))
 
 
+@_on_stream
 def chunk_fwd_reduced(q, k, v, log_alpha, beta, mode="kda", S0=None, output_final_state=True, stream=None):
     """o, S_T with reduced gates: mode 'kda' (beta [B,T,H] for both gates,
     log_alpha [B,T,H,dk]) or 'gdn' (also a scalar decay, log_alpha [B,T,H])."""
@@ -562,6 +607,7 @@ def chunk_fwd_reduced(q, k, v, log_alpha, beta, mode="kda", S0=None, output_fina
     return o, S_T
 
 
+@_on_stream
 def chunk_bwd_reduced(q, k, v, log_alpha, beta, S0, dO, dS_T=None, mode="kda", need_dS0=True, stream=None):
     """Gradients with reduced gates: dq, dk, dv, dlog_alpha (the shape of
     log_alpha), dbeta [B,T,H] and dS0."""
@@ -581,6 +627,7 @@ def chunk_bwd_reduced(q, k, v, log_alpha, beta, S0, dO, dS_T=None, mode="kda", n
     return g
 
 
+@_on_stream
 def decode_step_reduced(q, k, v, log_alpha, beta, S, mode="kda", stream=None):
     """o = one decode step with reduced gates (beta [B,H]; 'gdn': log_alpha [B,H]); S updated in place."""
     import torch
@@ -593,6 +640,7 @@ def decode_step_reduced(q, k, v, log_alpha, beta, S, mode="kda", stream=None):
     return o
 
 
+@_on_stream
 def prologue(xq, xk, xv, Wq, Wk, Wv, xa, xb, xw, cu_seqlens=None, stream=None):
     """The mixer's inputs (q, k, v, log_alpha, b, w) from the projections and
     gate pre-activations: token tensors [B, T, H, D] (or packed [T, H, D] with
@@ -609,6 +657,7 @@ def prologue(xq, xk, xv, Wq, Wk, Wv, xa, xb, xw, cu_seqlens=None, stream=None):
     return dict(zip(("q", "k", "v", "log_alpha", "b", "w"), outs))
 
 
+@_on_stream
 def prologue_bwd(xq, xk, xv, Wq, Wk, Wv, xa, xb, xw, grads, cu_seqlens=None, stream=None):
     """Gradients of the prologue's inputs from `grads` (dq, dk, dv, dlog_alpha, db, dw)."""
     import torch
@@ -630,6 +679,7 @@ def prologue_bwd(xq, xk, xv, Wq, Wk, Wv, xa, xb, xw, grads, cu_seqlens=None, str
     return dx
 
 
+@_on_stream
 def output_gate(o, g, gamma, stream=None):
     """z = o / rms(o) * gamma * silu(g) per token and head (o, g [..., H, dv], gamma fp32 [dv])."""
     import torch
@@ -640,6 +690,7 @@ def output_gate(o, g, gamma, stream=None):
     return z
 
 
+@_on_stream
 def output_gate_bwd(o, g, gamma, dz, stream=None):
     """(do, dg, dgamma) of output_gate."""
     import torch
@@ -653,6 +704,7 @@ def output_gate_bwd(o, g, gamma, dz, stream=None):
     return dO, dg, dgamma
 
 
+@_on_stream
 def chunk_fwd_gated(q, k, v, log_alpha, b, w, g, gamma, S0=None, output_final_state=True, stream=None):
     """z, S_T: the forward with the output epilogue z = o / rms(o) * gamma * silu(g)."""
     import torch
@@ -675,11 +727,6 @@ def chunk_fwd_gated(q, k, v, log_alpha, b, w, g, gamma, S0=None, output_final_st
 # A single token's call is over in microseconds, so these checks are written to
 # cost little: shapes and strides are read once, and contiguous tensors take a
 # short way.
-#
-# stream= (a torch stream or a raw handle): the call runs, and allocates what it
-# returns, as if that stream were the current one.  The caller orders it behind
-# the making of its inputs, keeps these alive until it has run, and orders what
-# reads its outputs on another stream behind it.
 
 
 def _elsewhere(t):
@@ -690,24 +737,6 @@ def _elsewhere(t):
     if i < 0:
         raise ValueError("tensors must be CUDA tensors, got one on %s" % t.device)
     return i != torch._C._cuda_getDevice()
-
-
-def _there(fn, t, stream, *args, **kw):
-    """fn(*args, **kw) with t's device current and, where one is given, `stream`
-    (a torch stream or a handle) as its current stream.  What the call allocates
-    then comes from that stream's own memory pool: a block of the calling
-    stream's pool may still be in use by work that stream has pending, and
-    nothing orders the call behind it."""
-    import torch
-    with torch.cuda.device(t.device):
-        if stream is None:
-            return fn(*args, **kw)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        if stream.device != t.device:
-            raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
 
 
 def _raw_stream(t):

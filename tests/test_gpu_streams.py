@@ -47,8 +47,41 @@ def ssm_calls(g):
     }
 
 
+def mixer_calls(g):
+    gen = torch.Generator().manual_seed(113)
+    r = lambda *s: torch.randn(*s, generator=gen).to("cuda", torch.bfloat16)  # noqa: E731
+    B, T, H, D = 2, 150, 2, 128
+    unit = lambda t: torch.nn.functional.normalize(t, dim=-1)  # noqa: E731
+    q, k, v, w, dO = unit(r(B, T, H, D)), unit(r(B, T, H, D)), r(B, T, H, D), r(B, T, H, D).sigmoid(), r(B, T, H, D)
+    la, b, beta = -r(B, T, H, D).abs(), r(B, T, H, D).sigmoid(), r(B, T, H).sigmoid()
+    S0 = 0.1 * torch.randn(B, H, D, D, generator=gen).cuda()
+    x, x1 = (q, k, v, la, b, w), [t[:, 0].contiguous() for t in (q, k, v, la, b, w)]
+    cu = torch.tensor([0, 40, B * T], dtype=torch.int32, device="cuda")
+    flat = [t.flatten(0, 1) for t in x]
+    W, gamma = [torch.randn(H * D, 4, generator=gen).cuda() for _ in range(3)], torch.ones(D, device="cuda")
+    states, fstates = g.chunk_fwd(*x, S0, save_states=True)[2], g.chunk_fwd_varlen(*flat, cu, S0, save_states=True)[2]
+    grads = {"d" + n: t for n, t in zip(("q", "k", "v", "log_alpha", "b", "w"), (dO,) * 6)}
+    return {
+        "chunk_fwd": lambda **s: g.chunk_fwd(*x, S0, save_states=True, **s),
+        "chunk_bwd": lambda **s: g.chunk_bwd(*x, S0, dO, **s),
+        "chunk_bwd, states": lambda **s: g.chunk_bwd(*x, S0, dO, states=states, **s),
+        "decode_step": lambda **s: g.decode_step(*x1, S0.clone(), **s),
+        "chunk_fwd_varlen": lambda **s: g.chunk_fwd_varlen(*flat, cu, S0, save_states=True, **s),
+        "chunk_bwd_varlen": lambda **s: g.chunk_bwd_varlen(*flat, cu, S0, dO.flatten(0, 1), states=fstates, **s),
+        "chunk_fwd_reduced": lambda **s: g.chunk_fwd_reduced(q, k, v, la, beta, S0=S0, **s),
+        "chunk_bwd_reduced": lambda **s: g.chunk_bwd_reduced(q, k, v, la, beta, S0, dO, **s),
+        "decode_step_reduced": lambda **s: g.decode_step_reduced(*x1[:4], beta[:, 0].contiguous(), S0.clone(), **s),
+        "prologue": lambda **s: g.prologue(q, k, v, *W, la, b, w, **s),
+        "prologue_bwd": lambda **s: g.prologue_bwd(q, k, v, *W, la, b, w, grads, **s),
+        "output_gate": lambda **s: g.output_gate(v, w, gamma, **s),
+        "output_gate_bwd": lambda **s: g.output_gate_bwd(v, w, gamma, dO, **s),
+        "chunk_fwd_gated": lambda **s: g.chunk_fwd_gated(*x, w, gamma, S0, **s),
+    }
+
+
+@pytest.mark.parametrize("calls", [ssm_calls, mixer_calls])
 @pytest.mark.parametrize("handle", [False, True])
-def test_outputs_and_workspace_are_of_the_streams_pool(handle, monkeypatch):
+def test_outputs_and_workspace_are_of_the_streams_pool(handle, calls, monkeypatch):
     import gated_delta_rule_gdn2_b200 as g
     from gated_delta_rule_gdn2_b200 import binding
     side, work = torch.cuda.Stream(), []
@@ -59,7 +92,7 @@ def test_outputs_and_workspace_are_of_the_streams_pool(handle, monkeypatch):
         return work[-1]
 
     monkeypatch.setattr(binding, "_scratch", spy)
-    for name, call in ssm_calls(g).items():
+    for name, call in calls(g).items():
         del work[:]
         torch.cuda.synchronize()
         out = tensors(call(stream=side.cuda_stream if handle else side))
@@ -70,12 +103,12 @@ def test_outputs_and_workspace_are_of_the_streams_pool(handle, monkeypatch):
     assert torch.cuda.current_stream() != side and g.gdn2_get_device_status() == 0
 
 
-def test_a_call_elsewhere_right_behind_one_here():
+@pytest.mark.parametrize("make_calls", [ssm_calls, mixer_calls])
+def test_a_call_elsewhere_right_behind_one_here(make_calls):
     """Without a wait between them, as often as not with what the call before
     has just given back."""
     import gated_delta_rule_gdn2_b200 as g
-    calls = ssm_calls(g)
-    del calls["ssm_step"], calls["ssm_prologue_step"]  # (their states are made on the current stream)
+    calls = {n: f for n, f in make_calls(g).items() if "step" not in n}  # (those make their states on the current stream)
     want = {n: tensors(f()) for n, f in calls.items()}
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
@@ -89,9 +122,10 @@ def test_a_call_elsewhere_right_behind_one_here():
                 assert torch.equal(x, y) and torch.equal(x, z), n
 
 
-def test_a_stream_of_another_device_is_refused():
+@pytest.mark.parametrize("calls", [ssm_calls, mixer_calls])
+def test_a_stream_of_another_device_is_refused(calls):
     import gated_delta_rule_gdn2_b200 as g
     other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
-    for n, f in ssm_calls(g).items():
+    for n, f in calls(g).items():
         with pytest.raises(ValueError):
             f(stream=other)
