@@ -8,20 +8,23 @@
 // G = q k^T kept once per CTA and D_ij the decay from j to i, a head is
 //     X = v dO^T            -> W = G D X: sums for dla and ddt; Z += D X dt
 // over both of its units, and a unit
+//     R = q S               -> u_i += e^{L_i} R_i . dO_i
 //     Y = k E               -> r_j += w_j Y_j . v_j; Y scaled by w_j
 //     Y += (G D)^T dO       -> dv = dt Y + skip dO
-//     dq += (e^L dO) S^T    -> u_i = q_i . (what the head added)
+//     dq += (e^L dO) S^T
 //     dk += (dt w v) E^T
 // and behind the last head dq += Z k, dk += Z^T q, so that both are summed over
 // the heads before they are rounded.  Rows of X, Y are tokens j (lanes of
 // tensor memory), columns i, so that (G D)^T is written back to tensor memory
 // as the left operand of the third product; the sums over j of W's columns are
-// a transposing reduction within each warp.  Operands rounded to bf16: G, G D,
+// a transposing reduction within each warp.  (u_i is also q_i . (what the head
+// adds to dq_i), but as a difference of sums over the heads it would have the
+// rounding of the largest of them.)  Operands rounded to bf16: G, G D,
 // e^L dO, dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
 //
 // Bound: 64 KB in and 16 KB out a unit at dk = 128 (3500 cycles of an SM's share
-// of HBM) against 1500 cycles of tensor pipe.  Measured 8300 cycles a unit (8 x
-// 4096 tokens, 16 heads of 128: 281 us; 256 blocks, so a wave and three
+// of HBM) against 1500 cycles of tensor pipe.  Measured 8800 cycles a unit (8 x
+// 4096 tokens, 16 heads of 128: 299 us; 256 blocks, so a wave and three
 // quarters), 48% of the issue slots: X's elementwise part is the longest
 // stretch, for its rows j <= i lie four blocks deep in the first sub-partition
 // of tensor memory and one deep in the last, and only a sub-partition's own
@@ -29,7 +32,8 @@
 // instructions and products issued by a converged warp 501 -> 436 us; the
 // diagonal block without branches 393; no registers spilled 369; dq in tensor
 // memory, which frees 32 registers a thread, 331; X and u once a head 295; no
-// warp waits for the next head's decays as they are loaded 281.
+// warp waits for the next head's decays as they are loaded 281; u from R 299
+// (with <E, S> ahead of R 310; Y's part ahead of X's 322).
 #include "common.cuh"
 #include "ssm_tc.cuh"
 
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                        idZq = tc::idesc_bf16(128, N, true, true);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t ld_qk, ldx[2], ld[2], b_x, b_y, b_c, b_d, b_z;
+    __shared__ uint64_t ld_qk, ldx[2], ld[2], b_x, b_q, r_q, b_y, b_c, b_d, b_z;
     __shared__ uint32_t tmem_slot;
     __shared__ int dead;
     BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
@@ -140,8 +144,9 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
 
     if (warp == kIssuer) tc::tmem_alloc(&tmem_slot, 512);
     if (tid == 0) {
-        uint64_t *bars[] = {&ld_qk, &ldx[0], &ldx[1], &ld[0], &ld[1], &b_x, &b_y, &b_c, &b_d, &b_z};
+        uint64_t *bars[] = {&ld_qk, &ldx[0], &ldx[1], &ld[0], &ld[1], &b_x, &b_q, &b_y, &b_c, &b_d, &b_z};
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
+        tc::mbar_init(&r_q, kNT / 32);
         tc::fence_mbar_init();
         dead = 0;
     }
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     }
     handoff();
 
-    float Z[32], es = 0.f, dsk = 0.f, rs = 0.f, q_dq = 0.f;  // rs: r of token j = row; q_dq: q . dq up to the head before
+    float Z[32], es = 0.f, dsk = 0.f, rs = 0.f, us = 0.f;  // rs, us: r and u of the token `row`
 #pragma unroll
     for (int i = 0; i < 32; ++i) Z[i] = 0.f;
 
@@ -269,8 +274,13 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         mma_tiles<true, true>(tm + cX, v, kCT, v + L::VB, kCT, 4, idX, u % NX > 0);
         if (u % NX == NX - 1) tc::commit(&b_x);
     };
-    auto product_Y = [&](int u) {
+    auto product_R = [&](int u) {  // (lies where Y comes next)
         wait(&ld[u & 1], (uint32_t)(u >> 1) & 1u);
+        if (!elect()) return;
+        mma_tiles<true, false>(tm + cY, sm + L::Q, kCT, sm + L::ST0 + (u & 1) * L::STAGE + 2 * L::VB + L::SB, N, N / 16, idY, false);
+        tc::commit(&b_q);
+    };
+    auto product_Y = [&](int u) {
         if (!elect()) return;
         mma_tiles<true, false>(tm + cY, sm + L::K, kCT, sm + L::ST0 + (u & 1) * L::STAGE + 2 * L::VB, N, N / 16, idY, false);
         tc::commit(&b_y);
@@ -280,7 +290,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
             wait(&ldx[0], 0);
             product_X(0);
         }
-        product_Y(0);
+        product_R(0);
     }
     for (int u = 0; u < nu && !aborted; ++u) {
         const int s = u & 1, hh = u / NX, x = u % NX, h = h_lo + hh;
@@ -304,6 +314,44 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         wait(&ld[s], ph2);
         const float dtj = G.dt[row];
+        if (x == 0 && u > 0) {  // the head before is summed up; its parts may be overwritten
+            if (NX == 1) asm volatile("bar.sync 2, 512;\n" ::: "memory");
+            else if (p == 3) asm volatile("bar.sync 1, 128;\n" ::: "memory");  // (the other warps wait for X, which comes after)
+            if (warp == kFinisher) finish(hh - 1);  // (this warp has no part in X below)
+        }
+        if (!tail && NX > 1 && x == 0 && warp == kIssuer) {  // the rest of X
+            wait(&ldx[1], ph2);
+            product_X(u + 1);
+        }
+        // ---- R: token i = row, value columns 16 qc ..
+        wait(&b_q, ph);
+        tc::fence_after();
+        {
+            float r[16];
+            ld16(tl + cY + 16 * qc, r);
+            const float er = G.er[row];
+            float d = 0.f;
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(sO + piece(kCT, row, 2 * qc + i));
+                const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 oo = unpack2(oe[e]);
+                    d = fmaf(r[8 * i + 2 * e], oo.x, fmaf(r[8 * i + 2 * e + 1], oo.y, d));
+                }
+            }
+            us = fmaf(er, d, us);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&r_q);
+        if (warp == kIssuer) {  // (every warp has read R)
+            wait(&r_q, ph);
+            tc::fence_after();
+            product_Y(u);
+        }
         // <E, S> (the two images have one layout), by the warps with the least of X
         if (p >= 2) {
             const int t = (warp >> 2) * 64 + (p & 1) * 32 + lane;  // 0 .. 255
@@ -317,45 +365,6 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                     es = fmaf(y.x, z.x, fmaf(y.y, z.y, es));
                 }
             }
-        }
-        if (x == 0 && u > 0) {  // the head before is summed up; its parts may be overwritten
-            if (NX == 1) asm volatile("bar.sync 2, 512;\n" ::: "memory");
-            else if (p == 3) asm volatile("bar.sync 1, 128;\n" ::: "memory");  // (the other warps wait for X, which comes after)
-            if (warp == kFinisher) finish(hh - 1);  // (this warp has no part in X below)
-        }
-        if (!tail && NX > 1 && x == 0 && warp == kIssuer) {  // the rest of X
-            wait(&ldx[1], ph2);
-            product_X(u + 1);
-        }
-        // ---- Y: token j = row, value columns 16 qc ..  (v is overwritten: X has read this unit's before Y, or, behind a
-        // sequence's end, where it was issued after, is waited for)
-        if (tail && x == 0) wait(&b_x, hh & 1);
-        wait(&b_y, ph);
-        tc::fence_after();
-        {
-            float y[16];
-            ld16(tl + cY + 16 * qc, y);
-            const float w = G.wt[row], wd = w * dtj;
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t at = piece(kCT, row, 2 * qc + i);
-                const uint4 v = *reinterpret_cast<const uint4 *>(sV + at), o = *reinterpret_cast<const uint4 *>(sO + at);
-                uint32_t ve[4] = {v.x, v.y, v.z, v.w};
-                const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 vv = unpack2(ve[e]), oo = unpack2(oe[e]);
-                    const int c = 8 * i + 2 * e;
-                    dsk = fmaf(vv.x, oo.x, fmaf(vv.y, oo.y, dsk));
-                    y[c] *= w;
-                    y[c + 1] *= w;
-                    rs = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, rs));
-                    ve[e] = pack2(vv.x * wd, vv.y * wd);
-                }
-                *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
-            }
-            stw<16>(tl + cY + 16 * qc, y);
         }
         // ---- X of the head: token j = row, tokens i = 32 qc ..; (G D)^T over the columns read
         if (x == 0) {
@@ -441,8 +450,36 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 }
             }
             st8(tl + cX + 32 * qc + 16, eo);
-            tc::wait_st();
         }
+        // ---- Y: token j = row, value columns 16 qc ..  (v is overwritten: X, which has read it, was waited for above)
+        wait(&b_y, ph);
+        tc::fence_after();
+        {
+            float y[16];
+            ld16(tl + cY + 16 * qc, y);
+            const float w = G.wt[row], wd = w * dtj;
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = piece(kCT, row, 2 * qc + i);
+                const uint4 v = *reinterpret_cast<const uint4 *>(sV + at), o = *reinterpret_cast<const uint4 *>(sO + at);
+                uint32_t ve[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t oe[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 vv = unpack2(ve[e]), oo = unpack2(oe[e]);
+                    const int c = 8 * i + 2 * e;
+                    dsk = fmaf(vv.x, oo.x, fmaf(vv.y, oo.y, dsk));
+                    y[c] *= w;
+                    y[c + 1] *= w;
+                    rs = fmaf(y[c], vv.x, fmaf(y[c + 1], vv.y, rs));
+                    ve[e] = pack2(vv.x * wd, vv.y * wd);
+                }
+                *reinterpret_cast<uint4 *>(sV + at) = make_uint4(ve[0], ve[1], ve[2], ve[3]);
+            }
+            stw<16>(tl + cY + 16 * qc, y);
+        }
+        tc::wait_st();
         if (x == NX - 1) {
             const float e2 = warp_sum(es), d2 = warp_sum(dsk);
             if (lane == 0) {
@@ -450,7 +487,8 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 red[16 + warp] = d2;
             }
             rp[qc][row] = rs;
-            es = dsk = rs = 0.f;
+            up[qc][row] = us;
+            es = dsk = rs = us = 0.f;
         }
         if (x == 0 && gt >= 0) {
             form_bwd_gates(gates[(hh + 1) & 1], bounded_log(__bfloat162float(g_la)), __bfloat162float(g_dt), gt);
@@ -493,29 +531,6 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
                 *reinterpret_cast<uint4 *>(sm + L::STG + at) = make_uint4(oe[0], oe[1], oe[2], oe[3]);
             }
         }
-        if (x == NX - 1) {  // u_i = q_i . (what the head added to dq_i): key channels WN qc ..
-            wait(&b_d, ph);
-            tc::fence_after();
-            float us = 0.f;
-#pragma unroll
-            for (int hf = 0; hf < WN / 16; ++hf) {
-                float t[16];
-                ld16(tl + cDQ + WN * qc + 16 * hf, t);
-                uint32_t qe[8];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4 *>(&qe[4 * i]) =
-                        *reinterpret_cast<const uint4 *>(sm + L::Q + piece(kCT, row, WN / 8 * qc + 2 * hf + i));
-                tc::wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 qq = unpack2(qe[e]);
-                    us = fmaf(qq.x, t[2 * e], fmaf(qq.y, t[2 * e + 1], us));
-                }
-            }
-            up[qc][row] = us - q_dq;
-            q_dq = us;
-        }
         if (warp == kIssuer) {
             wait(&b_d, ph);
             if (!tail && x == NX - 1 && u + 1 < nu) {  // the next X (the products that read (G D)^T and e^L dO are done)
@@ -525,7 +540,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         handoff();
         if (aborted) break;
-        if (warp == kIssuer && u + 1 < nu) product_Y(u + 1);
+        if (warp == kIssuer && u + 1 < nu) product_R(u + 1);
         if (warp == kFinisher) {
             if (u + 2 < nu) load(u + 2);  // (the stage's products and reads are done)
             if (!tail && elect()) {

@@ -23,10 +23,13 @@ def copies(lens, G, dk, dv, dtype):
     return n
 
 
-def check(lens, H, G, dk, dv, dtype, packed, save=True):
+def check(lens, H, G, dk, dv, dtype, packed, save=True, scale=None):
     import gated_delta_rule_gdn2_b200 as g
     T, B = sum(lens), len(lens)
     x = make(B, T, H, G, dk, dv, dtype, lens=lens, seed=121 + H)
+    if scale is not None:  # heads of uneven size
+        x["dO"] = x["dO"] * scale[:, None]
+        x["dS_T"] = x["dS_T"] * scale[:, None, None]
     if packed:
         n = copies(lens, G, dk, dv, dtype)
     else:
@@ -81,3 +84,14 @@ def test_every_head_of_a_block(T, H, G, dk, dv, dtype):
                                             ((129, 64), 6, 2, 64, 128)])
 def test_every_head_of_a_packed_block(lens, H, G, dk, dv, dtype):
     check(lens, H, G, dk, dv, dtype, True, save=H != 5)
+
+
+@pytest.mark.parametrize("dtype", SCAN)
+@pytest.mark.parametrize("lens,H,dk,dv", [((100, 100), 3, 128, 128), ((200, 200), 4, 64, 64), ((90, 150), 3, 128, 64)])
+def test_a_large_head_leaves_the_others_digits(lens, H, dk, dv, dtype):
+    """A head whose gradients are 2^20 times the others': theirs are as near as
+    without it, whichever head of the block it is."""
+    for at in (0, H - 1):
+        scale = torch.ones(H, dtype=F64)
+        scale[at] = 2.0 ** 20
+        check(lens, H, 1, dk, dv, dtype, lens[0] != lens[1], scale=scale)
