@@ -74,17 +74,25 @@ __device__ __forceinline__ void store(T *p, const float (&v)[V]) {
 
 // 1 / (1 + e^{-x}): 0 and 1 at the ends (e^{-x} = inf divides to 0)
 __device__ __forceinline__ float sigm(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-// Of two values by one reciprocal: their denominators stay below 2^58 (a
-// sigmoid that leaves out is under 2^-57, and only ever a factor of values of x's size).
-__device__ __forceinline__ float2 sigm2(float2 x) {
+// Of two values.  (One reciprocal of the product of both denominators would have
+// to keep e^{-x} below 2^64, where a sigmoid is far from 0 against an x of 1e15;
+// a branch around it costs the forward 6%.)  rest: 1 - sigmoid, which for large x
+// is not the difference: s is rounded, and the derivative multiplies what is left
+// by x.  Where s is 0 it is of no account, but must not be a NaN.
+__device__ __forceinline__ float2 sigm2(float2 x, float2 &rest) {
     const float2 t = __fmul2_rn(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
-    float2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e.x) : "f"(fminf(t.x, 57.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e.y) : "f"(fminf(t.y, 57.f)));
+    float2 e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e.y) : "f"(t.y));
     const float2 a = __fadd2_rn(e, make_float2(1.f, 1.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(a.x * a.y));
-    return __fmul2_rn(make_float2(r, r), make_float2(a.y, a.x));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(s.x) : "f"(a.x));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(s.y) : "f"(a.y));
+    rest = __fmul2_rn(make_float2(fminf(e.x, 3e38f), fminf(e.y, 3e38f)), s);
+    return s;
+}
+__device__ __forceinline__ float2 sigm2(float2 x) {
+    float2 rest;
+    return sigm2(x, rest);
 }
 // log(1 + e^x) without cancellation or overflow
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
@@ -381,9 +389,10 @@ __device__ __forceinline__ void conv_strip_bwd(const ProArgs &a, int c, long lon
 #pragma unroll
                 for (int j = 0; j < K; ++j)
                     u = __ffma2_rn(make_float2(w[j][i], w[j][i + 1]), make_float2(win[j][i], win[j][i + 1]), u);
-                const float2 s = sigm2(u);
-                du[i] = g[i] * s.x * fmaf(u.x, 1.f - s.x, 1.f);
-                du[i + 1] = g[i + 1] * s.y * fmaf(u.y, 1.f - s.y, 1.f);
+                float2 n;
+                const float2 s = sigm2(u, n);
+                du[i] = g[i] * s.x * fmaf(u.x, n.x, 1.f);
+                du[i + 1] = g[i + 1] * s.y * fmaf(u.y, n.y, 1.f);
             }
             const float own_row = decltype(inside)::value || at < own ? 1.f : 0.f;
 #pragma unroll
