@@ -74,6 +74,8 @@ int copy_state(float *dst, const float *src, int B, int H, int dk, int dv, cudaS
 }  // namespace
 
 int *device_status_ptr() { return status_ptr(); }
+uint32_t debug_wait_limit() { return g_wait_limit; }
+int debug_withheld() { return g_withhold_ready; }
 
 }  // namespace gdn2
 

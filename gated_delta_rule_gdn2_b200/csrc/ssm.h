@@ -13,6 +13,8 @@ namespace gdn2 {
 
 int *device_status_ptr();  // (api.cu) the status word of the current device, nullptr on failure
 int device_sm_count();     // SMs of the current device
+uint32_t debug_wait_limit();  // (api.cu) the test knobs' values: iterations of a wait (0: the default),
+int debug_withheld();         // and the chunk whose hand-over does not come (-1: none)
 
 namespace ssm {
 
@@ -96,6 +98,8 @@ struct ScanArgs {
     int parts;
     float *part_state, *part_decay;
     bool sorted;        // (bf16) blocks take the sequences by length, longest first
+    uint32_t wait_limit;  // (bf16) the test knobs
+    int withheld;
 };
 
 struct ScanBwdArgs {

@@ -160,6 +160,8 @@ int gdn2_ssm_fwd(const void *q, const void *k, const void *v, const void *log_al
     if (ws_bytes < p.total || (p.total && !ws)) return GDN2_ERR_WORKSPACE;
     ScanArgs a{q, k, v, log_alpha, dt, skip, S0, o, S_T, states, ldq, ldk, ldv, cu_seqlens, B, T, H, G,
                device_status_ptr(), p.parts};
+    a.wait_limit = debug_wait_limit();
+    a.withheld = debug_withheld();
     if (!a.status) return GDN2_ERR_CUDA;
     unsigned char *w = static_cast<unsigned char *>(ws);
     a.part_state = reinterpret_cast<float *>(w + p.part_state);
@@ -195,6 +197,8 @@ int gdn2_ssm_bwd(const void *q, const void *k, const void *v, const void *log_al
                    ldq, ldk, ldv, cu_seqlens, B, T, H, G, device_status_ptr(), p.parts,
                    reinterpret_cast<float *>(w + p.part_state), reinterpret_cast<float *>(w + p.part_decay)};
     if (!a.f.status) return GDN2_ERR_CUDA;
+    a.f.wait_limit = debug_wait_limit();
+    a.f.withheld = debug_withheld();
     a.dO = dO; a.dS_T = dS_T; a.dq = dq; a.dk = dk_; a.dv = dv_; a.dla = dlog_alpha; a.ddt = ddt;
     a.dskip = dskip; a.dS0 = dS0; a.grads = w + p.grads; a.splits = p.splits;
     a.dqk_part = reinterpret_cast<float *>(w + p.dqk);

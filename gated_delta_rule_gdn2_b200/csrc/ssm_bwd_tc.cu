@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t ld_qk, ldx[2], ld[2], b_x, b_q, r_q, b_y, b_c, b_d, b_z;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead;
+    __shared__ Waits waits;
     BwdGates *gates = reinterpret_cast<BwdGates *>(sm + L::G);
     float(*rowp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::ROWP), (*colp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::COLP);
     float(*rp)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::RP), (*up)[kCT] = reinterpret_cast<float(*)[kCT]>(sm + L::UP);
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         for (uint64_t *x : bars) tc::mbar_init(x, 1);
         tc::mbar_init(&r_q, kNT / 32);
         tc::fence_mbar_init();
-        dead = 0;
+        waits_init(waits, a.f.wait_limit);
     }
     tc::fence_before();
     __syncthreads();
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     };
     bool bad = false, aborted = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!wait_bar(bar, parity, &dead)) bad = true;
+        if (!wait_bar(bar, parity, &waits)) bad = true;
         __syncwarp();
     };
     auto handoff = [&]() {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&r_q);
+        if (lane == 0 && u != f.withheld) tc::mbar_arrive(&r_q);
         if (warp == kIssuer) {  // (every warp has read R)
             wait(&r_q, ph);
             tc::fence_after();
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     }
     tc::fence_before();
     __syncthreads();
-    if (tid == 0 && dead) record_status(f.status, GDN2_ERR_TIMEOUT);
+    if (tid == 0 && waits.dead) record_status(f.status, GDN2_ERR_TIMEOUT);
     if (warp == kIssuer) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     // tiles landed; products done; hand-overs of the groups (one arrival a warp)
     __shared__ uint64_t ld_qk[2], ld_v, d_g, d_yi, d_s1, d_s, d_y, r_hl, r_hl2, r_m, r_st, r_o, r_y2, r_tail, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead;
+    __shared__ Waits waits;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, half = (warp >> 2) & 1, row = 32 * p + lane;
     const int part = blockIdx.x % a.parts, i = blockIdx.x / a.parts, h = i % a.H, g = h / (a.H / a.G),
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
             tc::mbar_init(&r_gfree[i], 16);
         }
         tc::fence_mbar_init();
-        dead = 0;
+        waits_init(waits, a.wait_limit);
     }
     tc::fence_before();
     __syncthreads();
@@ -205,13 +205,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
 
     // a bounded wait by a whole warp, with one answer for all its lanes
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &dead)) != 0; };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &waits)) != 0; };
     // what this warp wrote, and read, handed over
-    auto give = [&](uint64_t *bar) {
+    auto give = [&](uint64_t *bar, bool comes = true) {
         tc::fence_async_smem();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar);
+        if (lane == 0 && comes) tc::mbar_arrive(bar);
     };
     auto tile_o = [&](int m) { return sm + (L::OVER_Q ? L::Q + (m & 1) * L::QB : L::O); };
     // chunk m's parity on a barrier that completes once a chunk, or once in R chunks
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
             give(&r_st);
             ok = ok && wait(&ld_v, 0);
             if (ok) start_y2();
-            give(&r_y2);
+            give(&r_y2, a.withheld != 0);
         }
         for (int m = 0; ok && m < n_chunks; ++m) {
             const uint32_t ph = m & 1;
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
                 give(&r_st);
                 if (!wait(&ld_v, ph ^ 1)) break;
                 start_y2();
-                give(&r_y2);
+                give(&r_y2, a.withheld != m + 1);
             } else if (last_part && a.S_T) {
 #pragma unroll 1
                 for (int x = 0; x < HP / 32; ++x) {
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(ScanArgs a, const _
     }
     tc::fence_before();
     __syncthreads();
-    if (tid == 0 && dead) record_status(a.status, GDN2_ERR_TIMEOUT);
+    if (tid == 0 && waits.dead) record_status(a.status, GDN2_ERR_TIMEOUT);
     if (warp == 16) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 512);
@@ -523,6 +523,8 @@ struct ChainArgs {
     float *part_state, *part_decay;
     int *status;
     bool sorted;
+    uint32_t wait_limit;
+    int withheld;
 };
 
 struct ChainMaps {
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, cons
     unsigned char *sm = smem_raw + ((1024u - (tc::smem_addr(smem_raw) & 1023u)) & 1023u);
     __shared__ uint64_t ld[2], d_s1, d_s, r_hl, r_hl2, r_st, r_gate[kRing], r_gfree[kRing], d_fin;
     __shared__ uint32_t tmem_slot;
-    __shared__ int dead;
+    __shared__ Waits waits;
     Gates *gates = reinterpret_cast<Gates *>(sm + L::G);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = warp & 3, half = (warp >> 2) & 1, row = 32 * p + lane;
     const int np = LOCAL ? a.parts - 1 : a.parts;
@@ -576,18 +578,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, cons
             tc::mbar_init(&r_gfree[i], LOCAL ? 8 : 16);
         }
         tc::fence_mbar_init();
-        dead = 0;
+        waits_init(waits, a.wait_limit);
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_slot, tl = tm + ((uint32_t)(32 * p) << 16);
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &dead)) != 0; };
-    auto give = [&](uint64_t *bar) {
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, &waits)) != 0; };
+    auto give = [&](uint64_t *bar, bool comes = true) {
         tc::fence_async_smem();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar);
+        if (lane == 0 && comes) tc::mbar_arrive(bar);
     };
     auto par = [](int m, int R) { return (uint32_t)(m / R) & 1u; };
 
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, cons
             give(&r_hl);
             if (m > 0 && !wait(&d_s, ph ^ 1)) break;
             scale_hi_lo<N, 256, 64>(A, sm + L::LO + L::AB / 2, f, 64, len, tid);
-            give(&r_hl2);
+            give(&r_hl2, a.withheld != m);
             if (lane == 0) tc::mbar_arrive(&r_gfree[m % kRing]);
         }
     } else {
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) chain_kernel(ChainArgs a, cons
     }
     tc::fence_before();
     __syncthreads();
-    if (tid == 0 && dead) record_status(a.status, GDN2_ERR_TIMEOUT);
+    if (tid == 0 && waits.dead) record_status(a.status, GDN2_ERR_TIMEOUT);
     if (warp == 16) {
         tc::fence_after();
         tc::tmem_dealloc(tm, 128);
@@ -741,7 +743,7 @@ cudaError_t go_chain(const ChainArgs &c, const ChainMaps &m, cudaStream_t s) {
 
 ChainArgs chain_args(const ScanArgs &a) {
     return ChainArgs{a.la, a.dt, nullptr, nullptr, nullptr, a.cu, a.B, a.T, a.H, a.G, a.parts, a.part_state, a.part_decay,
-                     a.status, by_length(a.cu, a.B, a.H, a.parts)};
+                     a.status, by_length(a.cu, a.B, a.H, a.parts), a.wait_limit, a.withheld};
 }
 
 template <int N, int P>

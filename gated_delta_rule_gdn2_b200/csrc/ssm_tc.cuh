@@ -50,20 +50,29 @@ __device__ __forceinline__ float exp_ftz(float x) {
     return y;
 }
 
+// What a block's bounded waits share (in shared memory).
+struct alignas(8) Waits {
+    uint32_t dead;   // one has run out
+    uint32_t limit;  // iterations of a wait
+};
+__device__ __forceinline__ void waits_init(Waits &w, uint32_t limit) {
+    w.dead = 0;
+    w.limit = limit ? limit : tc::kWaitLimit;
+}
 // A bounded wait for the phase `parity` of a barrier: false when it ran out
-// here, or (dead != 0) in any thread of the block.  Kept to a dozen
+// here, or (w->dead) in any thread of the block.  Kept to a dozen
 // instructions: the kernels hold dozens of waits, and their code has to stay
 // within the instruction cache.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *dead) {
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Waits *w) {
     uint32_t ok;
     asm volatile(
-        "{\n.reg .pred p;\n.reg .u32 n, d;\nmov.u32 n, 0;\n"
+        "{\n.reg .pred p;\n.reg .u32 n, d, l;\nmov.u32 n, 0;\n"
         "AGAIN:\n"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         "@p bra DONE;\n"
-        "ld.volatile.shared.u32 d, [%3];\n"
+        "ld.volatile.shared.v2.u32 {d, l}, [%3];\n"
         "add.u32 n, n, 1;\n"
-        "setp.ge.u32 p, n, %4;\n"
+        "setp.ge.u32 p, n, l;\n"
         "@p mov.u32 d, 1;\n"
         "setp.eq.u32 p, d, 0;\n"
         "@p bra AGAIN;\n"
@@ -72,7 +81,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *de
         "DONE:\n"
         "selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(tc::smem_addr(bar)), "r"(parity), "r"(tc::smem_addr(dead)), "n"(tc::kWaitLimit)
+        : "r"(tc::smem_addr(bar)), "r"(parity), "r"(tc::smem_addr(w))
         : "memory");
     return ok != 0;
 }

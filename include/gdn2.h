@@ -467,12 +467,19 @@ const char *gdn2_status_string(int status);
  * make a device-side bounded wait run out and check that the kernel gives
  * up cleanly, records GDN2_ERR_TIMEOUT and leaves the context usable.
  *   GDN2_DEBUG_WAIT_LIMIT: iterations of every bounded mbarrier wait of the
- *     chunk kernels launched from now on (0 = the default, a few seconds).
+ *     chunk kernels launched from now on (0 = the default, a few seconds),
+ *     the state space scan's bf16 kernels among them (but not the waits for
+ *     copies that have to land before a block may end).
  *   GDN2_DEBUG_WITHHOLD_READY: the chunk index at which the bf16
  *     dk = dv = 128 forward withholds the arrival that hands a chunk's
  *     intra-chunk results to its state chain (-1 = none, the default); the
  *     chain's wait for it then runs out.  No copy or tensor-core operation
  *     depends on that arrival, so the kernel ends with none of them in flight.
+ *     The state space scan's bf16 kernels withhold a hand-over at the chunk
+ *     walked as that number too (the forward: skip v for M v; the chains of
+ *     states and gradients: the second half of the scaled rows; the
+ *     backward, by units of 64 value columns: the read of R), with the same
+ *     outcome.
  * Host-global settings of the process, not for production use; returns
  * GDN2_OK or GDN2_ERR_INVALID_ARG.
  */
