@@ -830,9 +830,30 @@ def _scan_sizes(q, k, v, log_alpha, dt, skip, cu_seqlens, lead_dims):
     return hs, dev, B, T, H, G, dk, dv, ldq, ldk, ldv
 
 
-def _like_rows(t, ld):
-    """An empty tensor with t's shape and row distance."""
-    return _empty_as(t) if ld == t.shape[-2] * t.shape[-1] else t.new_empty_strided(t.shape, t.stride())
+def _like_rows(ts, lds):
+    """Empty tensors with the shapes and row distances of ts.  Those that are
+    separate slices of one tensor's rows become slices of one tensor again: each
+    with rows of its own, as far apart, would take that tensor's size."""
+    out, groups = [None] * len(ts), {}
+    for i, (t, ld) in enumerate(zip(ts, lds)):
+        if ld == t.shape[-2] * t.shape[-1]:
+            out[i] = _empty_as(t)
+        else:
+            groups.setdefault((t.untyped_storage().data_ptr(), ld), []).append(i)
+    for (_, ld), g in groups.items():
+        g.sort(key=lambda i: ts[i].storage_offset())
+        at = [ts[i].storage_offset() for i in g]
+        end = [a + ts[i].shape[-2] * ts[i].shape[-1] for a, i in zip(at, g)]
+        if len(g) == 1 or end[-1] - at[0] > ld or any(e > a for e, a in zip(end, at[1:])):
+            for i in g:
+                out[i] = ts[i].new_empty_strided(ts[i].shape, ts[i].stride())
+            continue
+        t = ts[g[0]]
+        rows = t.numel() // (t.shape[-2] * t.shape[-1])
+        both = t.new_empty((rows - 1) * ld + end[-1] - at[0])
+        for i, a in zip(g, at):
+            out[i] = both.as_strided(ts[i].shape, ts[i].stride(), a - at[0])
+    return out
 
 
 def ssm_fwd(q, k, v, log_alpha, dt, skip=None, S0=None, output_final_state=True, save_states=False, cu_seqlens=None,
@@ -870,7 +891,8 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
             into=None, stream=None):
     """Gradients (dq, dk, dv, dlog_alpha, ddt, dskip, dS0) of ssm_fwd from dO
     and dS_T.  `states` from ssm_fwd(..., save_states=True) on the same inputs
-    skips forming them anew.  dq, dk, dv have their input's strides; `into`
+    skips forming them anew.  dq, dk, dv have their input's strides (slices of
+    one tensor's rows: as slices of one new tensor); `into`
     (dq, dk, dv) gives the tensors to write them to, such as views of the
     prologue's dy."""
     if _elsewhere(q) or stream is not None:
@@ -889,7 +911,7 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
     for name, t, x, ld, w in zip(("dq", "dk", "dv"), into or (), (q, k, v), (ldq, ldk, ldv), (G * dk, G * dk, H * dv)):
         if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != dev or _row_ld(name, t, len(hs) - 1, w) != ld:
             raise ValueError("%s must have its input's shape, dtype and row stride" % name)
-    dq, dk_, dv_ = into or (_like_rows(q, ldq), _like_rows(k, ldk), _like_rows(v, ldv))
+    dq, dk_, dv_ = into or _like_rows((q, k, v), (ldq, ldk, ldv))
     g = {"dq": dq, "dk": dk_, "dv": dv_, "dlog_alpha": torch.empty_like(log_alpha), "ddt": torch.empty_like(dt),
          "dskip": None if skip is None else torch.empty_like(skip),
          "dS0": None}

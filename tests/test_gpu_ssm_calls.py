@@ -1,0 +1,34 @@
+"""Calls of the state space operators that the entry points allow and the other
+tests do not make."""
+import pytest
+import torch
+
+from test_gpu_ssm import GRADS, SCAN, TD, cu_of, dev, make
+from test_ssm_slices import slices
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", SCAN)
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_of_slices(dtype, packed):
+    """q, k, v as slices of one tensor's rows, the gradients where the call puts
+    them: as of contiguous copies, bit for bit."""
+    import gated_delta_rule_gdn2_b200 as g
+    H, G, dk, dv = 4, 2, 64, 128
+    lens = (90, 0, 111) if packed else None
+    d, cu = dev(make(3 if packed else 2, 201, H, G, dk, dv, dtype, lens=lens, seed=141), dtype), cu_of(lens)
+    wide = torch.zeros(*d["v"].shape[:-2], H * dv + 2 * G * dk + 64, dtype=TD[dtype], device="cuda")
+    views = slices(wide, H, G, dk, dv)
+    for t, n in zip(views, "qkv"):
+        t.copy_(d[n])
+    rest = (d["la"], d["dt"], d["dO"])
+    kw = dict(skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"], cu_seqlens=cu)
+    want = g.ssm_bwd(d["q"], d["k"], d["v"], *rest, **kw)
+    before = torch.cuda.memory_allocated()
+    got = g.ssm_bwd(*views, *rest, **kw)
+    small = sum(got[n].numel() * got[n].element_size() for n in ("dlog_alpha", "ddt", "dskip", "dS0"))
+    assert torch.cuda.memory_allocated() - before <= wide.numel() * wide.element_size() + small + (1 << 14)
+    for n in GRADS + ("dskip", "dS0"):
+        assert torch.equal(got[n], want[n]), n
+    assert g.gdn2_get_device_status() == 0
