@@ -234,7 +234,7 @@ template <int N, int P>
 struct BwdSmem {
     static constexpr int LN = N + 4, LP = P + 4, LG = 68;
     static constexpr int Q = 0, K = Q + 64 * LN, V = K + 64 * LN, O = V + 64 * LP, S = O + 64 * LP, M = S + N * LP,
-                         LAM = M + 64 * LG, LSU = LAM + 64, BS = LSU + 64, DT = BS + 4, RS = DT + 64, CSP = RS + 64, R = CSP + 8 * 64, UU = R + 64,
+                         LAM = M + 64 * LG, LML = LAM + 64, LSU = LML + 64, BS = LSU + 64, DT = BS + 4, RS = DT + 64, CSP = RS + 64, R = CSP + 8 * 64, UU = R + 64,
                          CD = UU + 64, RED = CD + 64, END = RED + 16;
     static constexpr size_t BYTES = sizeof(float) * END;
 };
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(256, N + P == 128 ? 2 : 1) chunk_bwd_kernel(Sc
     using L = BwdSmem<N, P>;
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm + L::Q, *sK = sm + L::K, *sV = sm + L::V, *sO = sm + L::O, *sS = sm + L::S, *sM = sm + L::M;
-    float *lam = sm + L::LAM, *lsu = sm + L::LSU, *bs = sm + L::BS, *sdt = sm + L::DT, *rs = sm + L::RS, *csp = sm + L::CSP, *sr = sm + L::R, *su = sm + L::UU,
+    float *lam = sm + L::LAM, *lml = sm + L::LML, *lsu = sm + L::LSU, *bs = sm + L::BS, *sdt = sm + L::DT, *rs = sm + L::RS, *csp = sm + L::CSP, *sr = sm + L::R, *su = sm + L::UU,
           *cd = sm + L::CD, *red = sm + L::RED;
     const ScanArgs &f = a.f;
     const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15, warp = tid >> 5;
@@ -389,24 +389,31 @@ __global__ void __launch_bounds__(256, N + P == 128 ? 2 : 1) chunk_bwd_kernel(Sc
             // from the block's start through the token, lsu = from behind it to the
             // block's end, bs = the block's.  An exponent L_i - L_j across blocks
             // is then a sum of terms <= 0, which loses nothing where a chunk
-            // decays far.
+            // decays far.  Within a block it is a difference of prefix sums, and
+            // behind a run of resets (kLogMin each) both are in the thousands: the
+            // prefix sums are formed in 64 bits and kept in two parts, lam + lml.
             const int t = 2 * tid;
             const size_t r = (row + t) * f.H + h;
             const float *la = static_cast<const float *>(f.la), *dt = static_cast<const float *>(f.dt);
             const float x0 = t < len ? bounded_log(la[r]) : 0.f, x1 = t + 1 < len ? bounded_log(la[r + f.H]) : 0.f;
-            float up = x0 + x1, dn = up;
+            double up = (double)x0 + x1;
+            float dn = x0 + x1;
 #pragma unroll
             for (int m = 1; m < 8; m <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, up, m, 8), z = __shfl_down_sync(0xffffffffu, dn, m, 8);
+                const double y = __shfl_up_sync(0xffffffffu, up, m, 8);
+                const float z = __shfl_down_sync(0xffffffffu, dn, m, 8);
                 if ((tid & 7) >= m) up += y;
                 if ((tid & 7) + m < 8) dn += z;
             }
-            const float before = __shfl_up_sync(0xffffffffu, up, 1, 8), after = __shfl_down_sync(0xffffffffu, dn, 1, 8);
-            lam[t] = ((tid & 7) ? before : 0.f) + x0;
-            lam[t + 1] = up;
+            const float after = __shfl_down_sync(0xffffffffu, dn, 1, 8);
+            const double before = __shfl_up_sync(0xffffffffu, up, 1, 8), first = ((tid & 7) ? before : 0.) + x0;
+            lam[t] = (float)first;
+            lml[t] = (float)(first - lam[t]);
+            lam[t + 1] = (float)up;
+            lml[t + 1] = (float)(up - lam[t + 1]);
             lsu[t + 1] = (tid & 7) < 7 ? after : 0.f;
             lsu[t] = lsu[t + 1] + x1;
-            if ((tid & 7) == 7) bs[tid >> 3] = up;
+            if ((tid & 7) == 7) bs[tid >> 3] = (float)up;
             sdt[t] = t < len ? dt[r] : 0.f;
             sdt[t + 1] = t + 1 < len ? dt[r + f.H] : 0.f;
         }
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(256, N + P == 128 ? 2 : 1) chunk_bwd_kernel(Sc
                     const int i = ti + 16 * r, j = tj + 16 * c;
                     // (r, c: the blocks of i and j)
                     const float mid = r == 2 && c == 0 ? b1 : r == 3 && c == 1 ? b2 : r == 3 && c == 0 ? b1 + b2 : 0.f;
-                    const float D = r > c ? expf(lam[i] + mid + lsu[j]) : r == c && i >= j ? expf(lam[i] - lam[j]) : 0.f;
+                    const float D = r > c ? expf(lam[i] + mid + lsu[j]) : r == c && i >= j ? expf((lam[i] - lam[j]) + (lml[i] - lml[j])) : 0.f;
                     const float x = X[r][c] * D, dtj = sdt[j], w = G[r][c] * x;
                     sM[i * L::LG + j] = G[r][c] * D;
                     Z[r][c] = fmaf(x, dtj, Z[r][c]);

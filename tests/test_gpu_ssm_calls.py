@@ -3,7 +3,9 @@ tests do not make."""
 import pytest
 import torch
 
-from test_gpu_ssm import GRADS, SCAN, TD, cu_of, dev, make
+import ssm_norms as N
+import ssm_ref as R
+from test_gpu_ssm import F64, GRADS, NAMES, SCAN, TD, check_all, cu_of, dev, make
 from test_ssm_slices import slices
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +34,22 @@ def test_gradients_of_slices(dtype, packed):
     for n in GRADS + ("dskip", "dS0"):
         assert torch.equal(got[n], want[n]), n
     assert g.gdn2_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", SCAN)
+@pytest.mark.parametrize("T,dk,dv", [(16, 64, 64), (64, 128, 64), (150, 128, 128)])
+def test_runs_of_resets(T, dk, dv, dtype):
+    """Twelve resets in each run of sixteen tokens, as in front of a padded
+    sequence's tokens: the four behind them see each other with all digits."""
+    import gated_delta_rule_gdn2_b200 as g
+    x = make(2, T, 2, 1, dk, dv, dtype, seed=151)
+    at = torch.arange(T) % 16 < 12
+    x["la"][:, at] = -1e4
+    x["la"] = x["la"].to(TD[dtype]).to(F64)
+    d = dev(x, dtype)
+    check_all(x, d, dtype)
+    ref = R.scan_grads(*[x[n] for n in NAMES], x["dO"], x["dS_T"])
+    a = [d[n] for n in ("q", "k", "v", "la", "dt")]
+    gr = g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"])
+    for n in GRADS:
+        N.close(n, gr[n].cpu(), ref[n], N.BF16 if dtype == "bf16" else N.FP32, 2)
