@@ -178,6 +178,8 @@ int gdn2_ssm_bwd(const void *q, const void *k, const void *v, const void *log_al
     if (st != GDN2_OK) return st;
     if (!o16(S0) || !o16(dS_T) || !o16(dS0) || !o16(states) || !o16(ws) || !of4(skip) || !of4(dskip) || !of4(cu_seqlens))
         return GDN2_ERR_INVALID_ARG;
+    // (the gradients of q and k are sums over heads, and there is none to write them)
+    if (H == 0 && B > 0 && T > 0) return GDN2_ERR_INVALID_ARG;
     if (B == 0 || H == 0 || T == 0) {
         if (dskip && H > 0) {
             const int e = launch_status(cudaMemsetAsync(dskip, 0, (size_t)H * 4, stream));

@@ -368,7 +368,8 @@ int gdn2_output_gate_bwd(const void *o, const void *g, const float *gamma, const
  * larger workspace (states_given = 0 in its query).  The workspace queries
  * take the same sizes, with packed != 0 for a packed batch, and hold for the
  * device that is current; no workspace may be shared by calls that overlap.
- * An empty sequence hands its state through; T = 0 likewise.
+ * An empty sequence hands its state through; T = 0 likewise.  The backward
+ * refuses H = 0 where there are tokens (GDN2_ERR_INVALID_ARG).
  *
  * gdn2_ssm_step: one token per sequence, rows [B], S updated in place.
  */
