@@ -20,11 +20,14 @@
 // a transposing reduction within each warp.  (u_i is also q_i . (what the head
 // adds to dq_i), but as a difference of sums over the heads it would have the
 // rounding of the largest of them.)  Operands rounded to bf16: G, G D,
-// e^L dO, dt w v, Z, and the images of S and E; sums are fp32, in a fixed order.
+// e^L dO, dt w v, and the images of S and E, all of them factors of gradients that
+// are rounded to bf16 themselves (dq and dk are 1.7e-3 of their norms from exact,
+// dv, dla and ddt 2.0e-3 to 2.3e-3, and that last rounding alone is 1.7e-3), and Z
+// in two parts; sums are fp32, in a fixed order.
 //
 // Bound: 64 KB in and 16 KB out a unit at dk = 128 (3500 cycles of an SM's share
-// of HBM) against 1500 cycles of tensor pipe.  Measured 8800 cycles a unit (8 x
-// 4096 tokens, 16 heads of 128: 299 us; 256 blocks, so a wave and three
+// of HBM) against 1500 cycles of tensor pipe.  Measured 9200 cycles a unit (8 x
+// 4096 tokens, 16 heads of 128: 301 us at 1965 MHz; 256 blocks, so a wave and three
 // quarters), 48% of the issue slots: X's elementwise part is the longest
 // stretch, for its rows j <= i lie four blocks deep in the first sub-partition
 // of tensor memory and one deep in the last, and only a sub-partition's own
@@ -33,7 +36,7 @@
 // diagonal block without branches 393; no registers spilled 369; dq in tensor
 // memory, which frees 32 registers a thread, 331; X and u once a head 295; no
 // warp waits for the next head's decays as they are loaded 281; u from R 299
-// (with <E, S> ahead of R 310; Y's part ahead of X's 322).
+// (with <E, S> ahead of R 310; Y's part ahead of X's 322); Z in two parts 301.
 #include "common.cuh"
 #include "ssm_tc.cuh"
 
@@ -570,15 +573,25 @@ __global__ void __launch_bounds__(kNT, 1) bwd_kernel(ScanBwdArgs a, const __grid
     __syncthreads();
     if (!aborted && nu > 0 && warp == kFinisher) finish(nh - 1);
 
-    // ---- dq += Z k, dk += Z^T q, and out
+    // ---- dq += Z k, dk += Z^T q, and out.  Z in two bf16 parts: where the heads
+    // of a group are cut into runs, each rounds its own Z, which may be far larger
+    // than what the group's sum is (one part: dq off by a tenth of its norm where
+    // pairs of heads cancel to a thirtieth).
+    unsigned char *Zhi = sm + L::ST0, *Zlo = Zhi + kCT * kCT * 2;
+    static_assert(2 * L::STAGE >= 2 * kCT * kCT * 2, "Z's parts lie over the stages");
     if (!aborted) {
-        put_row<32>(sm + L::ST0, kCT, row, 32 * qc, Z);
+        put_row<32>(Zhi, kCT, row, 32 * qc, Z);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) Z[i] -= __bfloat162float(__float2bfloat16_rn(Z[i]));
+        put_row<32>(Zlo, kCT, row, 32 * qc, Z);
     }
     handoff();
     if (!aborted) {
         if (warp == kIssuer && elect()) {
-            mma_tiles<true, false>(tm + cDK, sm + L::ST0, kCT, sm + L::Q, kCT, kCT / 16, idZk, nu > 0);
-            mma_tiles<false, false>(tm + cDQ, sm + L::ST0, kCT, sm + L::K, kCT, kCT / 16, idZq, nu > 0);
+            mma_tiles<true, false>(tm + cDK, Zhi, kCT, sm + L::Q, kCT, kCT / 16, idZk, nu > 0);
+            mma_tiles<true, false>(tm + cDK, Zlo, kCT, sm + L::Q, kCT, kCT / 16, idZk, true);
+            mma_tiles<false, false>(tm + cDQ, Zhi, kCT, sm + L::K, kCT, kCT / 16, idZq, nu > 0);
+            mma_tiles<false, false>(tm + cDQ, Zlo, kCT, sm + L::K, kCT, kCT / 16, idZq, true);
             tc::commit(&b_z);
         }
         wait(&b_z, 1);

@@ -53,3 +53,24 @@ def test_runs_of_resets(T, dk, dv, dtype):
     gr = g.ssm_bwd(*a, d["dO"], skip=d["skip"], S0=d["S0"], dS_T=d["dS_T"])
     for n in GRADS:
         N.close(n, gr[n].cpu(), ref[n], N.BF16 if dtype == "bf16" else N.FP32, 2)
+
+
+@pytest.mark.parametrize("B", [2, 150])
+@pytest.mark.parametrize("T,dk,dv", [(1, 64, 128), (3, 128, 64), (100, 128, 128), (128, 64, 64)])
+def test_heads_that_all_but_cancel(T, dk, dv, B):
+    """Heads in pairs whose shares of dq and dk differ by a thirtieth or less:
+    within a chunk without a state before it or a gradient behind, both are the sums of the heads'
+    (v . dO) times k or q, and keep their digits, in one block and in one a head."""
+    import gated_delta_rule_gdn2_b200 as g
+    x = make(2, T, 16, 1, dk, dv, "bf16", s0=False, seed=161)
+    near = 1 + 2.0 ** -5 * torch.rand(2, T, 8, dv, generator=torch.Generator().manual_seed(162), dtype=F64)
+    for n in ("v", "dt", "la"):
+        x[n][:, :, 1::2] = x[n][:, :, ::2]
+    x["dO"][:, :, 1::2] = (-x["dO"][:, :, ::2] * near).to(torch.bfloat16).to(F64)
+    d = {n: None if t is None or n in ("S0", "dS_T") else t if n == "skip" else t.repeat(B // 2, *[1] * (t.dim() - 1))
+         for n, t in dev(x, "bf16").items()}
+    gr = g.ssm_bwd(*[d[n] for n in ("q", "k", "v", "la", "dt")], d["dO"], skip=d["skip"])
+    ref = R.scan_grads(*[x[n] for n in NAMES], x["dO"], x["dS_T"])
+    for n in ("dq", "dk"):
+        N.close(n, gr[n][:2].cpu(), ref[n], N.BF16, 2)
+        assert torch.equal(gr[n], gr[n][:2].repeat(B // 2, 1, 1, 1))
