@@ -26,10 +26,11 @@
 // in two parts; sums are fp32, in a fixed order.
 //
 // Bound: 64 KB in and 16 KB out a unit at dk = 128 (3500 cycles of an SM's share
-// of HBM) against 1500 cycles of tensor pipe.  Measured 9200 cycles a unit (8 x
-// 4096 tokens, 16 heads of 128: 301 us at 1965 MHz; 256 blocks, so a wave and three
-// quarters), 48% of the issue slots: X's elementwise part is the longest
-// stretch, for its rows j <= i lie four blocks deep in the first sub-partition
+// of HBM) against 1500 cycles of tensor pipe.  Measured 8700 cycles a unit (8 x
+// 4096 tokens, 16 heads of 128: 302 us; 256 blocks, so a wave and three
+// quarters), with 46% of the issue slots, 19% of the tensor pipe and a quarter of
+// HBM in use: what bounds it is that the warps meet twice a unit and wait for
+// the longest stretch between.  That is X's elementwise part, for its rows j <= i lie four blocks deep in the first sub-partition
 // of tensor memory and one deep in the last, and only a sub-partition's own
 // warps can read it.  Kept on measurement (same case): waits of a dozen
 // instructions and products issued by a converged warp 501 -> 436 us; the

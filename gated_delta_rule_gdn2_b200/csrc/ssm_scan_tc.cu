@@ -16,14 +16,23 @@
 // E <- e^{L_end} E + sum_i e^{L_i} q_i do_i^T has the same form, walked from the
 // end.
 //
+// What is rounded to bf16 is so because an operand beside v or k, which are bf16,
+// has to be: M and the state's copy, which are factors of o alone.  o is rounded
+// to bf16 itself, which puts it 1.66e-3 of its norm from the exact one; with these
+// two it is 1.88e-3.  The state is not rounded; S_T is 1.3e-6 to 1.9e-6 of its norm
+// from exact by what the two parts leave out (fp32 products: 5e-8), and a third
+// part would be half as much again of the state's products and of the scaling.
+// The decay factors come from the fast base-2 exponential and logarithm: 2^-21.
+//
 // Bounds, at dk = dv = 128 and for a chunk: 64 KB of HBM traffic (v in, o out; q
 // and k come from L2, shared by the group's heads) take 2800 cycles of an SM's
 // share; the products take 2560 cycles of the tensor pipe, and read 256 KB of
 // operands from shared memory at its full 128 bytes a cycle; the warps and the
 // copies move another 350 KB through it.  So shared memory, at about 4800
-// cycles, bounds the chunk; measured 6700 (8 x 4096 tokens, 16 heads: 125 us
-// against 46 for the bytes at the rate of a plain copy).  What made the
-// difference on the way (same case): all warps in step 208 us; roles that meet
+// cycles, is the nearest limit; measured 7800 (8 x 4096 tokens, 16 heads: 130 to
+// 139 us, by the GPU, against 46 for the bytes at the rate of a plain copy), the
+// rest being the hand-overs between the roles.  What made the
+// difference on the way (same case, on the fastest GPU): all warps in step 208 us; roles that meet
 // through mbarriers, without local memory 174; waits of a dozen instructions
 // and products issued by a converged warp (the code had outgrown the
 // instruction cache) 150; separate accumulators for q S and M v, o's tile over
