@@ -391,7 +391,8 @@ def _there(fn, t, stream, *args, **kw):
         if stream is None:
             return fn(*args, **kw)
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
+            # (a handle of 0 is the default stream; torch would make a stream of its own of it)
+            stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
         if stream.device != t.device:
             raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
         with torch.cuda.stream(stream):
@@ -894,7 +895,7 @@ def ssm_bwd(q, k, v, log_alpha, dt, dO, skip=None, S0=None, dS_T=None, states=No
     skips forming them anew.  dq, dk, dv have their input's strides (slices of
     one tensor's rows: as slices of one new tensor); `into`
     (dq, dk, dv) gives the tensors to write them to, such as views of the
-    prologue's dy."""
+    prologue's dy, which may not overlap one another."""
     if _elsewhere(q) or stream is not None:
         return _there(ssm_bwd, q, stream, q, k, v, log_alpha, dt, dO, skip, S0, dS_T, states, need_dS0, cu_seqlens, into)
     import torch

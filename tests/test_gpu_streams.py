@@ -129,3 +129,22 @@ def test_a_stream_of_another_device_is_refused(calls):
     for n, f in calls(g).items():
         with pytest.raises(ValueError):
             f(stream=other)
+
+
+@pytest.mark.parametrize("calls", [ssm_calls, mixer_calls])
+def test_the_default_stream_by_its_handle(calls):
+    """stream=0, with another stream current, and the current one by its own handle."""
+    import gated_delta_rule_gdn2_b200 as g
+    fs = {n: f for n, f in calls(g).items() if "step" not in n}  # (those make their states on the current stream)
+    want = {n: tensors(f()) for n, f in fs.items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for handle in (0, side.cuda_stream):
+            for n, f in fs.items():
+                out = tensors(f(stream=handle))
+                torch.cuda.synchronize()
+                for x, y in zip(want[n], out):
+                    assert torch.equal(x, y), n
+                    assert not y.numel() or pool_of(y) == handle, n
+        assert torch.cuda.current_stream() == side
